@@ -23,6 +23,8 @@ MK_ERR_BOUNDS = -9
 MK_ABL_STREAM, MK_ABL_GRAPH, MK_ABL_PDL = 0, 1, 2
 MK_WEIGHTS_BF16, MK_WEIGHTS_INT8 = 0, 1
 
+MK_SRC_BF16, MK_SRC_F32 = 0, 1
+
 OP_NAMES = {0: "HALT", 1: "QKV", 2: "ATTN", 3: "OPROJ", 4: "MLP", 5: "LMHEAD", 6: "ROUTER", 8: "MLP_UP", 9: "MLP_DOWN", 10: "NORM",
             7: "NOP"}
 
@@ -71,6 +73,21 @@ class mk_plan_stats(C.Structure):
                [("max_sm_bytes", C.c_double), ("mean_sm_bytes", C.c_double)]
 
 
+class mk_kv_view(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p)] + \
+               [(n, C.c_int) for n in ("n_blocks", "n_kv_heads", "block", "head_dim")] + \
+               [("d_table", C.c_void_p), ("table_stride", C.c_int)]
+
+
+class mk_kv_batch(C.Structure):
+    _fields_ = [("batch", C.c_int), ("n_tokens", C.c_int), ("d_lens", C.c_void_p),
+                ("d_cu", C.c_void_p)]
+
+
+class mk_rows(C.Structure):
+    _fields_ = [("p", C.c_void_p), ("token_stride", C.c_long), ("head_stride", C.c_long)]
+
+
 class MkError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
@@ -105,6 +122,17 @@ SIGNATURES = {
     "mk_set_stage_bytes": (C.c_int, [C.c_void_p, C.c_int]),
     "mk_set_ring_depth": (C.c_int, [C.c_void_p, C.c_int]),
     "mk_set_kv_pages": (C.c_int, [C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_int]),
+    "mk_kv_append": (C.c_int, [C.POINTER(mk_kv_view), C.POINTER(mk_kv_batch), C.c_int,
+                               C.POINTER(mk_rows), C.POINTER(mk_rows), C.POINTER(mk_rows), C.c_int,
+                               C.POINTER(mk_rows), C.c_double, C.c_void_p]),
+    "mk_attn_decode": (C.c_int, [C.POINTER(mk_kv_view), C.POINTER(mk_kv_batch), C.c_int,
+                                 C.POINTER(mk_rows), C.c_float, C.POINTER(mk_rows), C.c_void_p,
+                                 C.c_void_p, C.c_size_t, C.c_void_p]),
+    "mk_attn_prefill": (C.c_int, [C.POINTER(mk_kv_view), C.POINTER(mk_kv_batch), C.c_int,
+                                  C.POINTER(mk_rows), C.c_float, C.POINTER(mk_rows), C.c_void_p,
+                                  C.c_void_p, C.c_size_t, C.c_void_p]),
+    "mk_attn_workspace_bytes": (C.c_int, [C.c_int] * 6 + [C.POINTER(C.c_size_t)]),
+    "mk_kv_status": (C.c_int, [C.c_void_p]),
     "mk_set_race_stress": (C.c_int, [C.c_void_p, C.c_uint, C.c_uint, C.c_int]),
     "mk_debug_read": (C.c_int, [C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_size_t]),
     "mk_set_poll_policy": (C.c_int, [C.c_void_p, C.c_int, C.c_uint]),
@@ -122,6 +150,8 @@ def lib():
     """Load libmk.so (building it in-tree first if it is missing or stale); with
     MK_LIB=bounds in the environment, the bounds-checked libmk_bounds.so."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB_BOUNDS if os.environ.get("MK_LIB") == "bounds" else _build.LIB
@@ -253,6 +283,37 @@ def mk_debug_read(h, what: int, layer: int, out) -> None:
 def mk_set_race_stress(h, max_delay_ns: int, seed: int, permute_queues: bool):
     _check(lib().mk_set_race_stress(h, int(max_delay_ns), int(seed), int(bool(permute_queues))),
            "mk_set_race_stress")
+
+
+def mk_kv_append(kv: mk_kv_view, bt: mk_kv_batch, n_q_heads: int, q, k: mk_rows, v: mk_rows,
+                 src_type: int, q_out, rope_theta: float, stream=None):
+    """q and q_out: mk_rows, or None with n_q_heads 0."""
+    _check(lib().mk_kv_append(kv, bt, n_q_heads, q, k, v, src_type, q_out, rope_theta, stream),
+           "mk_kv_append")
+
+
+def mk_attn_decode(kv: mk_kv_view, bt: mk_kv_batch, n_q_heads: int, q: mk_rows, scale: float,
+                   out: mk_rows, d_lse, d_ws, ws_bytes: int, stream=None):
+    _check(lib().mk_attn_decode(kv, bt, n_q_heads, q, scale, out, d_lse, d_ws, ws_bytes, stream),
+           "mk_attn_decode")
+
+
+def mk_attn_prefill(kv: mk_kv_view, bt: mk_kv_batch, n_q_heads: int, q: mk_rows, scale: float,
+                    out: mk_rows, d_lse, d_ws, ws_bytes: int, stream=None):
+    _check(lib().mk_attn_prefill(kv, bt, n_q_heads, q, scale, out, d_lse, d_ws, ws_bytes, stream),
+           "mk_attn_prefill")
+
+
+def mk_attn_workspace_bytes(decode: bool, n_tokens: int, batch: int, n_q_heads: int,
+                            n_kv_heads: int, head_dim: int) -> int:
+    n = C.c_size_t()
+    _check(lib().mk_attn_workspace_bytes(int(decode), n_tokens, batch, n_q_heads, n_kv_heads,
+                                         head_dim, C.byref(n)), "mk_attn_workspace_bytes")
+    return n.value
+
+
+def mk_kv_status(stream=None) -> int:
+    return lib().mk_kv_status(stream)
 
 
 def mk_set_kv_pages(h, block: int, n_blocks: int, d_table, table_stride: int):

@@ -25,7 +25,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmk.so")
 LIB_BOUNDS = os.path.join(PKG, "libmk_bounds.so")
 # translation units of the bounds-checked library (the small variant only)
-BOUNDS_CU = ("api.cu", "pack.cu", "k_h256_d64_g2_b1.cu")
+BOUNDS_CU = ("api.cu", "pack.cu", "kv_ops.cu", "k_h256_d64_g2_b1.cu")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,

@@ -1,0 +1,198 @@
+// kv_ops.cu -- the KV-cache operators' entry points: checks of the arguments,
+// choice of the kernel, launch.  No state, no allocation.
+#include <cmath>
+
+#include <cuda_runtime.h>
+
+#include "kv_append.cuh"
+#include "kv_attn_row.cuh"
+
+namespace mk {
+
+struct AttnArgs {
+  KvView kv;
+  KvBatch bt;
+  Rows q, o;
+  float* lse;
+  float scale;
+  int Hq;
+};
+
+// One warp per (token, query head).
+template <int D>
+__global__ void __launch_bounds__(128) kv_attn_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int t = (int)(w / a.Hq), hq = (int)(w % a.Hq);
+  if (t >= a.bt.n_tokens) return;
+  const int b = kv_seq_of_token(a.bt, t, lane);
+  if (b >= a.bt.batch) return;
+  const int after = a.bt.cu ? __ldg(a.bt.cu + b + 1) - t : 1;
+  const int n = max(0, kv_len(a.kv, a.bt, b) - after + 1);
+  float m, l, o[E];
+  attn_row<D>(a.kv, b, hq / (a.Hq / a.kv.Hkv), (const uint16_t*)a.q.p + t * a.q.ts + hq * a.q.hs,
+              a.scale, 0, n, m, l, o);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint16_t* dst = (uint16_t*)a.o.p + t * a.o.ts + hq * a.o.hs + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e++) dst[e] = to_bf16(l == 0.f ? 0.f : o[e] * inv);
+  if (a.lse && lane == 0) a.lse[(long long)t * a.Hq + hq] = l == 0.f ? -INFINITY : m + logf(l);
+}
+
+// ------------------------------------------------------- argument checks ----
+static bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// Rows of D elements of `size` bytes, each on a 16-byte boundary.
+static bool rows_ok(const mk_rows* r, size_t size) {
+  return r && r->p && aligned(r->p, 16) && (r->token_stride * (long)size) % 16 == 0 &&
+         (r->head_stride * (long)size) % 16 == 0;
+}
+
+static Rows rows(const mk_rows* r) { return Rows{r->p, r->token_stride, r->head_stride}; }
+
+// Fills the device structs; MK_OK, or why not.
+static int check(const mk_kv_view* kv, const mk_kv_batch* bt, KvView& v, KvBatch& b) {
+  if (!kv || !bt) return MK_ERR_INVALID_ARG;
+  if (!kv->k || !kv->v || !aligned(kv->k, 16) || !aligned(kv->v, 16) || kv->n_blocks < 1 ||
+      kv->n_kv_heads < 1 || kv->block < 1)
+    return MK_ERR_INVALID_ARG;
+  if (bt->batch < 0 || bt->n_tokens < 0 || (bt->batch > 0 && !bt->d_lens) ||
+      (!bt->d_cu && bt->n_tokens != bt->batch))
+    return MK_ERR_INVALID_ARG;
+  int shift = 0;
+  if (kv->d_table) {
+    if (kv->block < 16 || kv->block > 4096 || (kv->block & (kv->block - 1)) || kv->table_stride < 1)
+      return MK_ERR_INVALID_ARG;
+    while ((1 << shift) < kv->block) shift++;
+  } else if (kv->n_blocks < bt->batch) {
+    return MK_ERR_INVALID_ARG;
+  }
+  if (kv->head_dim != 64 && kv->head_dim != 128) return MK_ERR_UNSUPPORTED;
+  v = KvView{(const uint16_t*)kv->k, (const uint16_t*)kv->v, kv->d_table, kv->table_stride,
+             kv->n_blocks, kv->n_kv_heads, kv->block, shift,
+             kv->d_table ? (long long)kv->table_stride * kv->block : kv->block};
+  b = KvBatch{bt->d_lens, bt->d_cu, bt->batch, bt->n_tokens};
+  return MK_OK;
+}
+
+static int launched() { return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA; }
+
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" int mk_kv_append(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q_heads,
+                            const mk_rows* q, const mk_rows* k, const mk_rows* v, int src_type,
+                            const mk_rows* q_out, double rope_theta, void* stream) {
+  AppendArgs a;
+  const int rc = check(kv, bt, a.kv, a.bt);
+  if (rc) return rc;
+  if (src_type != MK_SRC_BF16 && src_type != MK_SRC_F32) return MK_ERR_INVALID_ARG;
+  const size_t size = src_type == MK_SRC_F32 ? 4 : 2;
+  if (n_q_heads < 0 || !(rope_theta == 0.0 || (rope_theta >= 1.0 && rope_theta <= 1e30)))
+    return MK_ERR_INVALID_ARG;
+  if (bt->n_tokens == 0 || bt->batch == 0) return MK_OK;
+  if (!rows_ok(k, size) || !rows_ok(v, size) ||
+      (n_q_heads > 0 && (!rows_ok(q, size) || !rows_ok(q_out, 2))))
+    return MK_ERR_INVALID_ARG;
+  a.k = rows(k);
+  a.v = rows(v);
+  if (n_q_heads > 0) {
+    a.q = rows(q);
+    a.qo = rows(q_out);
+  } else {
+    a.q = a.qo = Rows{};
+  }
+  a.Hq = n_q_heads;
+  a.rotate = rope_theta != 0.0;
+  const int D = kv->head_dim;
+  if (a.rotate) {
+    // theta^(-2t/D) / 2 pi as a fraction of 2^64, from the powers of two of t
+    double pw[6];
+    for (int i = 0; i < 6; i++) pw[i] = std::pow(rope_theta, -2.0 * (1 << i) / D);
+    for (int t = 0; t < D / 2; t++) {
+      double f = 0.15915494309189533577;  // 1 / 2 pi
+      for (int i = 0; i < 6; i++)
+        if (t & (1 << i)) f *= pw[i];
+      a.freq[t] = (unsigned long long)std::ldexp(f, 64);
+    }
+  }
+  const unsigned grid = (unsigned)((bt->n_tokens + KV_APPEND_TOKENS - 1) / KV_APPEND_TOKENS);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (D == 64) {
+    if (size == 4) kv_append_kernel<64, true><<<grid, KV_APPEND_THREADS, 0, s>>>(a);
+    else kv_append_kernel<64, false><<<grid, KV_APPEND_THREADS, 0, s>>>(a);
+  } else {
+    if (size == 4) kv_append_kernel<128, true><<<grid, KV_APPEND_THREADS, 0, s>>>(a);
+    else kv_append_kernel<128, false><<<grid, KV_APPEND_THREADS, 0, s>>>(a);
+  }
+  return launched();
+}
+
+extern "C" int mk_attn_workspace_bytes(int decode, int n_tokens, int batch, int n_q_heads,
+                                       int n_kv_heads, int head_dim, size_t* bytes) {
+  if (!bytes || decode < 0 || decode > 1 || n_tokens < 0 || batch < 0 || n_q_heads < 1 ||
+      n_kv_heads < 1 || n_q_heads % n_kv_heads)
+    return MK_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return MK_ERR_UNSUPPORTED;
+  *bytes = 0;
+  return MK_OK;
+}
+
+static int attention(bool decode, const mk_kv_view* kv, const mk_kv_batch* bt, int n_q_heads,
+                     const mk_rows* q, float scale, const mk_rows* out, float* d_lse, void* d_ws,
+                     size_t ws_bytes, void* stream) {
+  AttnArgs a;
+  const int rc = check(kv, bt, a.kv, a.bt);
+  if (rc) return rc;
+  if ((bt->d_cu != nullptr) == decode) return MK_ERR_INVALID_ARG;
+  size_t need = 0;
+  const int wrc = mk_attn_workspace_bytes(decode, bt->n_tokens, bt->batch, n_q_heads,
+                                          kv->n_kv_heads, kv->head_dim, &need);
+  if (wrc) return wrc;
+  if (bt->n_tokens == 0 || bt->batch == 0) return MK_OK;
+  if (!rows_ok(q, 2) || !rows_ok(out, 2) || (d_lse && !aligned(d_lse, 4)) ||
+      (need > 0 && (!d_ws || !aligned(d_ws, 256) || ws_bytes < need)))
+    return MK_ERR_INVALID_ARG;
+  a.q = rows(q);
+  a.o = rows(out);
+  a.lse = d_lse;
+  a.scale = scale;
+  a.Hq = n_q_heads;
+  const long long warps = (long long)bt->n_tokens * n_q_heads;
+  if (warps > (1ll << 32)) return MK_ERR_UNSUPPORTED;
+  const unsigned grid = (unsigned)((warps + 3) / 4);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (kv->head_dim == 64) kv_attn_kernel<64><<<grid, 128, 0, s>>>(a);
+  else kv_attn_kernel<128><<<grid, 128, 0, s>>>(a);
+  return launched();
+}
+
+extern "C" int mk_attn_decode(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q_heads,
+                              const mk_rows* q, float scale, const mk_rows* out, float* d_lse,
+                              void* d_ws, size_t ws_bytes, void* stream) {
+  return attention(true, kv, bt, n_q_heads, q, scale, out, d_lse, d_ws, ws_bytes, stream);
+}
+
+extern "C" int mk_attn_prefill(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q_heads,
+                               const mk_rows* q, float scale, const mk_rows* out, float* d_lse,
+                               void* d_ws, size_t ws_bytes, void* stream) {
+  return attention(false, kv, bt, n_q_heads, q, scale, out, d_lse, d_ws, ws_bytes, stream);
+}
+
+extern "C" int mk_kv_status(void* stream) {
+  cudaStream_t s = (cudaStream_t)stream;
+  int word = 0;
+  const int zero = 0;
+  if (cudaMemcpyFromSymbolAsync(&word, kv_status_word, sizeof(int), 0, cudaMemcpyDeviceToHost, s) !=
+          cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return MK_ERR_CUDA;
+  if (word != 0 &&
+      (cudaMemcpyToSymbolAsync(kv_status_word, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) !=
+           cudaSuccess ||
+       cudaStreamSynchronize(s) != cudaSuccess))
+    return MK_ERR_CUDA;
+  return word;
+}

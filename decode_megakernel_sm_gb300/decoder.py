@@ -7,6 +7,7 @@ import ctypes as C
 import torch
 
 from . import _lib as L
+from .cache import KVCache
 
 
 def desc_from_config(cfg: dict, max_batch: int, max_seq: int) -> L.mk_model_desc:
@@ -114,6 +115,11 @@ class Decoder:
         n_blocks = self.kcache[0].shape[0]
         L.mk_set_kv_pages(self.h, block, n_blocks, _ptr(table, torch.int32), table.shape[1])
         self._kv_table = table  # kept alive: the kernel reads it every step
+
+    def cache(self, layer: int) -> KVCache:
+        """Layer `layer`'s cache, contiguous or paged as the handle reads it, for the
+        cache operators: fill it from a prompt, attend to it, then step on."""
+        return KVCache(self.kcache[layer], self.vcache[layer], getattr(self, "_kv_table", None))
 
     def debug_read(self, what: str, layer: int):
         """An intermediate of the most recent step as a float32 numpy array:

@@ -183,6 +183,106 @@ int mk_quantize_rows_int8(const void* d_w, long rows, int cols, int8_t* d_codes,
 int mk_set_kv_pages(mk_handle* h, int block, int n_blocks, const int32_t* d_table,
                     int table_stride);
 
+/* ---- KV-cache operators ---------------------------------------------------
+ * The decode step appends one token's keys and values and attends to the
+ * cache inside its own kernel.  These three calls do the same work on a cache
+ * on their own, for any number of new tokens: they fill the cache that
+ * mk_decode_step continues from (a prompt), and read it.  No handle is
+ * needed; the current device must be the one the pointers belong to.  All
+ * are asynchronous on `stream` and may be captured into a graph.
+ *
+ * mk_kv_view: one layer's cache, in the layouts of mk_kv / mk_set_kv_pages:
+ *   with d_table, k and v are pools [n_blocks][n_kv_heads][block][head_dim]
+ *     (block a power of two, 16..4096) and row p of sequence b lies in block
+ *     d_table[b * table_stride + p / block] at row p % block;
+ *   with d_table NULL they are [n_blocks][n_kv_heads][block][head_dim] with
+ *     sequence b's rows in entry b (n_blocks >= batch, block = max_seq >= 1).
+ *   bf16, 16-byte aligned; head_dim 64 or 128 (MK_ERR_UNSUPPORTED otherwise).
+ * mk_kv_batch: what is in the batch.  d_lens[b]: rows of sequence b's cache,
+ *   the new tokens' included.  d_cu: [batch + 1] offsets, sequence b's new
+ *   tokens are rows [d_cu[b], d_cu[b + 1]) of q, k, v and the outputs
+ *   (d_cu[0] = 0, non-decreasing, d_cu[batch] <= n_tokens; rows from
+ *   d_cu[batch] on are padding, neither read nor written); NULL: one new
+ *   token per sequence, row b (n_tokens == batch).  The last new token of
+ *   sequence b sits at position d_lens[b] - 1, the ones before it just below;
+ *   a token whose position would be negative is not appended, and attends to
+ *   nothing.
+ * mk_rows: rows [token][head][head_dim] at the given strides in elements; the
+ *   last dimension is dense, every row starts on a 16-byte boundary.
+ *
+ * Errors, all three: MK_ERR_INVALID_ARG (NULL or misaligned pointers, sizes
+ * or strides outside the above), MK_ERR_UNSUPPORTED, MK_ERR_CUDA.  Contents
+ * of d_lens, d_cu and d_table are checked on the device: a length below 0 or
+ * above what the view holds, or a block id outside [0, n_blocks) in a place
+ * that is used, touches nothing outside the buffers, leaves that sequence's
+ * outputs unspecified, and makes mk_kv_status() return MK_ERR_INVALID_ARG. */
+typedef struct {
+  void* k;
+  void* v;
+  int n_blocks, n_kv_heads, block, head_dim;
+  const int32_t* d_table;
+  int table_stride;
+} mk_kv_view;
+
+typedef struct {
+  int batch, n_tokens;
+  const int32_t* d_lens;
+  const int32_t* d_cu;
+} mk_kv_batch;
+
+typedef struct {
+  void* p;
+  long token_stride, head_stride;
+} mk_rows;
+
+/* Append: rotate the new tokens' queries and keys by their positions and write
+ * keys and values into the cache.  With p the token's position and
+ * f_t = rope_theta^(-2t / head_dim), the pair (x[t], x[t + head_dim/2])
+ * becomes (x[t] cos - x[t + head_dim/2] sin, x[t + head_dim/2] cos + x[t] sin)
+ * of p * f_t, as in the decode step; arithmetic in fp32, angles exact to fp32
+ * at any position, one rounding to bf16.  rope_theta 0: no rotation; else >= 1.
+ * src_type: the type of q, k and v, MK_SRC_BF16 or MK_SRC_F32.  q_out (bf16)
+ * receives the rotated queries; it may be q itself (bf16).  n_q_heads 0:
+ * there are none, q and q_out are ignored.  Two new tokens that name the same
+ * cache row (through a table that repeats a block) race.                   */
+#define MK_SRC_BF16 0
+#define MK_SRC_F32 1
+int mk_kv_append(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q_heads, const mk_rows* q,
+                 const mk_rows* k, const mk_rows* v, int src_type, const mk_rows* q_out,
+                 double rope_theta, void* stream);
+
+/* Attention of the batch's new tokens over the cache, which holds their keys
+ * and values already: with s_j = scale * q . k_j,
+ *   out = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = log sum_j exp(s_j)
+ * over the rows j <= p of the token's sequence (query head h reads kv head
+ * h / (n_q_heads / n_kv_heads)).  A token that attends to nothing gets out 0
+ * and lse -inf.  q and out are bf16; d_lse (fp32 [n_tokens][n_q_heads]) may
+ * be NULL.  Rows of the cache that a token does not attend to do not reach
+ * its output, whatever they hold.
+ *   mk_attn_decode: one new token per sequence (bt->d_cu NULL): each reads
+ *     all d_lens[b] rows.
+ *   mk_attn_prefill: any number of new tokens per sequence, causal.
+ * d_ws: device scratch of at least mk_attn_workspace_bytes() bytes, 256-byte
+ * aligned, for this call alone until it has run: calls that may overlap, and
+ * graphs that may replay at the same time, need their own.  Its contents do
+ * not matter before or after.                                              */
+int mk_attn_decode(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q_heads, const mk_rows* q,
+                   float scale, const mk_rows* out, float* d_lse, void* d_ws, size_t ws_bytes,
+                   void* stream);
+int mk_attn_prefill(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q_heads, const mk_rows* q,
+                    float scale, const mk_rows* out, float* d_lse, void* d_ws, size_t ws_bytes,
+                    void* stream);
+
+/* Scratch bytes of mk_attn_decode (decode 1) or mk_attn_prefill (decode 0)
+ * on the current device for these sizes.                                   */
+int mk_attn_workspace_bytes(int decode, int n_tokens, int batch, int n_q_heads, int n_kv_heads,
+                            int head_dim, size_t* bytes);
+
+/* Wait for `stream`, then return and clear what the KV-cache operators found
+ * on the current device since the last call (MK_OK, MK_ERR_INVALID_ARG or
+ * MK_ERR_TIMEOUT); one word for all streams.  Not during a capture.        */
+int mk_kv_status(void* stream);
+
 /* Diagnostics: an intermediate of the handle's most recent step
  * (mk_decode_step, mk_decode_step_host, or the last step of
  * mk_decode_steps; not the no-allocation call), copied to host memory as
