@@ -44,12 +44,6 @@ MK_DEV void load8(const void* base, long long off, float (&f)[8]) {
   }
 }
 
-MK_DEV uint32_t bf2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 MK_DEV void store8(uint16_t* p, const float (&f)[8]) {
   *(uint4*)p = make_uint4(bf2(f[0], f[1]), bf2(f[2], f[3]), bf2(f[4], f[5]), bf2(f[6], f[7]));
 }

@@ -12,6 +12,13 @@ __device__ int kv_status_word = 0;
 
 MK_DEV void kv_fail(int code) { atomicCAS(&kv_status_word, 0, code); }
 
+// Two floats rounded to bf16, the first in the low half.
+MK_DEV uint32_t bf2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 struct KvView {
   const uint16_t* k;
   const uint16_t* v;

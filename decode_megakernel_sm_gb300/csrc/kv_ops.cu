@@ -5,18 +5,9 @@
 #include <cuda_runtime.h>
 
 #include "kv_append.cuh"
-#include "kv_attn_row.cuh"
+#include "kv_decode.cuh"
 
 namespace mk {
-
-struct AttnArgs {
-  KvView kv;
-  KvBatch bt;
-  Rows q, o;
-  float* lse;
-  float scale;
-  int Hq;
-};
 
 // One warp per (token, query head).
 template <int D>
@@ -38,6 +29,55 @@ __global__ void __launch_bounds__(128) kv_attn_kernel(const __grid_constant__ At
 #pragma unroll
   for (int e = 0; e < E; e++) dst[e] = to_bf16(l == 0.f ? 0.f : o[e] * inv);
   if (a.lse && lane == 0) a.lse[(long long)t * a.Hq + hq] = l == 0.f ? -INFINITY : m + logf(l);
+}
+
+// Streaming multiprocessors of the current device, 0 on an error.
+static int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
+// Launch `kernel` so that it may start while the one before it in the stream
+// runs; it waits for that one itself (griddepcontrol.wait).
+template <typename... P>
+static cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block,
+                                    cudaStream_t s, P... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Query heads of one item of the decode kernel: 8 fill half of a tensor-core
+// tile and are enough for most group sizes; more share the cache's bytes.
+static int decode_tiles(int G) { return G <= 8 ? 1 : 2; }
+
+template <int D, int NT>
+static size_t decode_ws(int n_sm) {
+  using Sh = DecShape<D, NT>;
+  return (size_t)n_sm * Sh::BLOCKS * 2 * Sh::STATE * sizeof(float);
+}
+
+template <int D, int NT>
+static int decode_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
+  using Sh = DecShape<D, NT>;
+  const int grid = n_sm * Sh::BLOCKS;
+  const long long items = (long long)a.bt.batch * a.kv.Hkv * ((a.G + Sh::HB - 1) / Sh::HB);
+  if (items > 0x7FFFFFFFll) return MK_ERR_UNSUPPORTED;
+  kv_decode_kernel<D, NT><<<grid, DEC_THREADS, 0, s>>>(a);
+  if (launch_dependent(kv_decode_join_kernel<D, NT>, (unsigned)items, D / 2 * 4, s, a, grid) !=
+      cudaSuccess)
+    return MK_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
 
 // ------------------------------------------------------- argument checks ----
@@ -137,6 +177,12 @@ extern "C" int mk_attn_workspace_bytes(int decode, int n_tokens, int batch, int 
     return MK_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return MK_ERR_UNSUPPORTED;
   *bytes = 0;
+  if (decode) {
+    const int n = sm_count(), nt = decode_tiles(n_q_heads / n_kv_heads);
+    if (n == 0) return MK_ERR_CUDA;
+    *bytes = head_dim == 64 ? (nt == 1 ? decode_ws<64, 1>(n) : decode_ws<64, 2>(n))
+                            : (nt == 1 ? decode_ws<128, 1>(n) : decode_ws<128, 2>(n));
+  }
   return MK_OK;
 }
 
@@ -147,19 +193,29 @@ static int attention(bool decode, const mk_kv_view* kv, const mk_kv_batch* bt, i
   const int rc = check(kv, bt, a.kv, a.bt);
   if (rc) return rc;
   if ((bt->d_cu != nullptr) == decode) return MK_ERR_INVALID_ARG;
+  if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads) return MK_ERR_INVALID_ARG;
+  if (bt->n_tokens == 0 || bt->batch == 0) return MK_OK;
+  if (!rows_ok(q, 2) || !rows_ok(out, 2) || (d_lse && !aligned(d_lse, 4)))
+    return MK_ERR_INVALID_ARG;
   size_t need = 0;
   const int wrc = mk_attn_workspace_bytes(decode, bt->n_tokens, bt->batch, n_q_heads,
                                           kv->n_kv_heads, kv->head_dim, &need);
   if (wrc) return wrc;
-  if (bt->n_tokens == 0 || bt->batch == 0) return MK_OK;
-  if (!rows_ok(q, 2) || !rows_ok(out, 2) || (d_lse && !aligned(d_lse, 4)) ||
-      (need > 0 && (!d_ws || !aligned(d_ws, 256) || ws_bytes < need)))
-    return MK_ERR_INVALID_ARG;
+  if (need > 0 && (!d_ws || !aligned(d_ws, 256) || ws_bytes < need)) return MK_ERR_INVALID_ARG;
   a.q = rows(q);
   a.o = rows(out);
   a.lse = d_lse;
   a.scale = scale;
   a.Hq = n_q_heads;
+  a.G = n_q_heads / kv->n_kv_heads;
+  a.ws = (float*)d_ws;
+  if (decode) {
+    const int n = sm_count(), nt = decode_tiles(a.G);
+    cudaStream_t s = (cudaStream_t)stream;
+    if (kv->head_dim == 64)
+      return nt == 1 ? decode_launch<64, 1>(a, n, s) : decode_launch<64, 2>(a, n, s);
+    return nt == 1 ? decode_launch<128, 1>(a, n, s) : decode_launch<128, 2>(a, n, s);
+  }
   const long long warps = (long long)bt->n_tokens * n_q_heads;
   if (warps > (1ll << 32)) return MK_ERR_UNSUPPORTED;
   const unsigned grid = (unsigned)((warps + 3) / 4);
