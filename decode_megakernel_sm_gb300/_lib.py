@@ -146,6 +146,9 @@ SIGNATURES = {
 }
 
 
+_SCALARS = (C.c_int, C.c_float, C.c_double, C.c_size_t)
+
+
 def lib():
     """Load libmk.so (building it in-tree first if it is missing or stale); with
     MK_LIB=bounds in the environment, the bounds-checked libmk_bounds.so."""
@@ -167,6 +170,16 @@ def lib():
                 f.argtypes = args
             _lib = L
     return _lib
+
+
+def packed(name: str):
+    """The entry point `name` for callers that pass its structures as packed bytes (in
+    the C layout): building a ctypes structure costs more than the call itself."""
+    L = lib()
+    f = L[name]  # a function object of its own, apart from lib().<name>
+    f.restype = C.c_int
+    f.argtypes = [t if t in _SCALARS else C.c_void_p for t in SIGNATURES[name][1]]
+    return f
 
 
 def lib_path() -> str:

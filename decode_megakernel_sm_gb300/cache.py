@@ -3,21 +3,27 @@ on the way), attend with one new token per sequence (decode) or with many
 (prefill).  Marshals torch CUDA tensors to the C ABI; no arithmetic here."""
 from __future__ import annotations
 
-import math
+import struct
 
 import torch
 
 from . import _lib as L
 
-_BF16 = torch.bfloat16
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+# The C structures as packed bytes, and the entry points that take them so.
+_VIEW = struct.Struct("=QQiiiiQi4x")  # mk_kv_view
+_BATCH = struct.Struct("=iiQQ")       # mk_kv_batch
+_ROWS = struct.Struct("=Qqq")         # mk_rows
+_entry = {}
+_scratch = {}  # scratch bytes by device, operator and sizes
 
 
-def _index(t, name, n, device):
-    """A dense int32 vector of n entries on the cache's device, as a pointer."""
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or t.device != device or \
-            not t.is_contiguous():
-        raise ValueError(f"{name}: expected {n} contiguous int32 values on {device}")
-    return t.data_ptr()
+def _call(name):
+    f = _entry.get(name)
+    if f is None:
+        f = _entry[name] = L.packed(name)
+    return f
 
 
 class KVCache:
@@ -38,68 +44,83 @@ class KVCache:
     kernels find in lens, cu and table (a length the cache cannot hold, a block
     outside the pool) is kept for ``check``."""
 
-    __slots__ = ("k", "v", "table", "device", "_view", "_ws")
+    __slots__ = ("k", "v", "table", "device", "heads", "dim", "held", "_index", "_view")
 
     def __init__(self, k, v, table=None):
-        if k.dim() != 4 or k.shape != v.shape or k.dtype != _BF16 or v.dtype != _BF16 or \
-                not k.is_cuda or v.device != k.device:
+        shape, device = k.shape, k.device
+        if len(shape) != 4 or v.shape != shape or k.dtype is not _BF16 or v.dtype is not _BF16 or \
+                not k.is_cuda or v.device != device:
             raise ValueError("k, v: expected two 4-dimensional bf16 CUDA tensors of one shape")
         if not (k.is_contiguous() and v.is_contiguous()):
             raise ValueError("k, v: expected contiguous tensors")
-        self.k, self.v, self.table, self.device = k, v, table, k.device
-        n_blocks, heads, block, dim = k.shape
+        n_blocks, self.heads, block, self.dim = shape
         if table is None:
-            tp, stride = None, 0
+            self.held, tp, stride = n_blocks, 0, 0
         else:
-            if table.dtype != torch.int32 or table.dim() != 2 or table.device != k.device or \
+            if table.dtype is not _I32 or table.dim() != 2 or table.device != device or \
                     not table.is_contiguous():
                 raise ValueError("table: expected a contiguous int32 matrix on the cache's device")
-            tp, stride = table.data_ptr(), table.shape[1]
-        self._view = L.mk_kv_view(k.data_ptr(), v.data_ptr(), n_blocks, heads, block, dim, tp,
-                                  stride)
-        self._ws = {}
+            self.held, stride = table.shape
+            tp = table.data_ptr()
+        self.k, self.v, self.table, self.device, self._index = k, v, table, device, device.index
+        self._view = _VIEW.pack(k.data_ptr(), v.data_ptr(), n_blocks, self.heads, block, self.dim,
+                                tp, stride)
 
     # -- marshalling --------------------------------------------------------
     def _rows(self, t, name, dtype, n=None, heads=None):
+        """mk_rows of t, which has to be [n][heads][dim] (None: any)."""
         s = t.shape
-        if len(s) != 3 or t.dtype != dtype or t.device != self.device or \
-                s[2] != self._view.head_dim or t.stride(2) != 1 or \
-                (n is not None and s[0] != n) or (heads is not None and s[1] != heads):
+        if len(s) != 3 or t.dtype is not dtype or t.get_device() != self._index or \
+                s[2] != self.dim or (n is not None and s[0] != n) or \
+                (heads is not None and s[1] != heads):
             raise ValueError(f"{name}: expected {dtype} [{'tokens' if n is None else n}]"
-                             f"[{'heads' if heads is None else heads}][{self._view.head_dim}] on "
-                             f"{self.device}, dense in the last dimension")
+                             f"[{'heads' if heads is None else heads}][{self.dim}] on {self.device}")
+        ts, hs, one = t.stride()
+        if one != 1:
+            raise ValueError(f"{name}: expected a dense last dimension")
         if t.requires_grad and torch.is_grad_enabled():
             raise ValueError(f"{name}: the cache operators have no backward pass")
         # the stride of a dimension of one means nothing
-        return L.mk_rows(t.data_ptr(), t.stride(0) if s[0] > 1 else 0,
-                         t.stride(1) if s[1] > 1 else 0)
+        return _ROWS.pack(t.data_ptr(), ts if s[0] > 1 else 0, hs if s[1] > 1 else 0)
+
+    def _vector(self, t, name, n):
+        if t.dtype is not _I32 or t.dim() != 1 or t.get_device() != self._index or \
+                (n is not None and t.shape[0] != n) or not t.is_contiguous():
+            raise ValueError(f"{name}: expected {'' if n is None else str(n) + ' '}contiguous int32 "
+                             f"values on {self.device}")
+        return t.data_ptr()
 
     def _batch(self, lens, cu, n):
-        batch = lens.shape[0] if lens.dim() == 1 else -1
-        held = self.k.shape[0] if self.table is None else self.table.shape[0]
-        if batch > held:
-            raise ValueError(f"lens: {batch} sequences in a cache of {held}")
-        lp = _index(lens, "lens", batch, self.device)
+        """(mk_kv_batch, batch)."""
+        lp = self._vector(lens, "lens", None)
+        batch = lens.shape[0]
+        if batch > self.held:
+            raise ValueError(f"lens: {batch} sequences in a cache of {self.held}")
         if cu is None:
             if n != batch:
                 raise ValueError(f"{n} tokens for {batch} sequences: pass cu")
-            return L.mk_kv_batch(batch, n, lp, None)
-        return L.mk_kv_batch(batch, n, lp, _index(cu, "cu", batch + 1, self.device))
+            return _BATCH.pack(batch, n, lp, 0), batch
+        return _BATCH.pack(batch, n, lp, self._vector(cu, "cu", batch + 1)), batch
 
-    def _on(self, stream, tensors, call):
-        """call(raw stream) with the cache's device and `stream` current."""
-        if stream is None and torch.cuda.current_device() == self.device.index:
-            return call(torch.cuda.current_stream().cuda_stream)
+    def _on(self, stream, tensors, call, *args):
+        """call(raw stream, *args) with the cache's device and `stream` current."""
+        if stream is None and torch.cuda.current_device() == self._index:
+            return call(torch._C._cuda_getCurrentRawStream(self._index), *args)
         with torch.cuda.device(self.device):
             if stream is None:
-                return call(torch.cuda.current_stream().cuda_stream)
+                return call(torch.cuda.current_stream().cuda_stream, *args)
             if not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(getattr(stream, "value", stream) or 0)
             for t in tensors:  # their memory is not reused before the stream is done with it
                 if t is not None:
                     t.record_stream(stream)
             with torch.cuda.stream(stream):
-                return call(stream.cuda_stream)
+                return call(stream.cuda_stream, *args)
+
+    def _dense(self, n, heads):
+        """A new bf16 [n][heads][dim] tensor and its mk_rows."""
+        t = torch.empty((n, heads, self.dim), dtype=_BF16, device=self.device)
+        return t, _ROWS.pack(t.data_ptr(), heads * self.dim, self.dim)
 
     # -- operators ----------------------------------------------------------
     def append(self, q, k, v, lens, cu=None, *, theta, q_out=None, stream=None):
@@ -111,61 +132,59 @@ class KVCache:
         [kv heads][head_dim]: all bf16 or all float32, any token and head strides
         that keep rows on 16-byte boundaries.  Returns the rotated queries, bf16
         (q_out if given; it may be q itself)."""
-        view, heads = self._view, self._view.n_kv_heads
-        n, src = k.shape[0], k.dtype
-        if src is not _BF16 and src is not torch.float32:
-            raise ValueError("k: expected bf16 or float32")
-        kr, vr = self._rows(k, "k", src, None, heads), self._rows(v, "v", src, n, heads)
-        bt = self._batch(lens, cu, n)
-        hq, qr = 0, None
+        src = k.dtype
+        if src is not _BF16 and src is not _F32:
+            raise ValueError("k: expected bfloat16 or float32")
+        kr = self._rows(k, "k", src, None, self.heads)
+        n = k.shape[0]
+        vr = self._rows(v, "v", src, n, self.heads)
+        bt, _ = self._batch(lens, cu, n)
+        hq, qr, given = 0, None, None
         if q is not None:
             qr, hq = self._rows(q, "q", src, n), q.shape[1]
-            given = None if q_out is None else self._rows(q_out, "q_out", _BF16, n, hq)
-        code = L.MK_SRC_F32 if src is torch.float32 else L.MK_SRC_BF16
+            if q_out is not None:
+                given = self._rows(q_out, "q_out", _BF16, n, hq)
+        return self._on(stream, (q, k, v, lens, cu, q_out, self.k, self.v, self.table),
+                        self._append, bt, n, hq, qr, kr, vr, int(src is _F32), q_out, given, theta)
 
-        def call(raw):
-            out, rows = q_out, None
-            if q is not None:
-                rows = given
-                if rows is None:
-                    out = torch.empty(q.shape, dtype=_BF16, device=self.device)
-                    rows = L.mk_rows(out.data_ptr(), hq * view.head_dim, view.head_dim)
-            L.mk_kv_append(view, bt, hq, qr, kr, vr, code, rows, theta, raw)
-            return out
-
-        return self._on(stream, (q, k, v, lens, cu, q_out, self.k, self.v, self.table), call)
+    def _append(self, raw, bt, n, hq, qr, kr, vr, src, out, rows, theta):
+        if qr is None:
+            out = None
+        elif rows is None:
+            out, rows = self._dense(n, hq)
+        status = _call("mk_kv_append")(self._view, bt, hq, qr, kr, vr, src, rows, theta, raw)
+        if status:
+            raise L.MkError(status, "mk_kv_append")
+        return out
 
     def _attend(self, decode, q, lens, cu, scale, out, return_lse, stream):
-        view = self._view
         qr = self._rows(q, "q", _BF16)
-        n, hq = q.shape[0], q.shape[1]
-        bt = self._batch(lens, cu, n)
+        n, hq, _ = q.shape
+        bt, batch = self._batch(lens, cu, n)
         given = None if out is None else self._rows(out, "out", _BF16, n, hq)
-        if scale is None:
-            scale = 1.0 / math.sqrt(view.head_dim)
-        key = (decode, n, bt.batch, hq)
-        need = self._ws.get(key)
+        key = (self._index, decode, n, batch, hq, self.heads, self.dim)
+        need = _scratch.get(key)
         if need is None:
-            need = L.mk_attn_workspace_bytes(decode, n, bt.batch, hq, view.n_kv_heads,
-                                             view.head_dim)
-            if len(self._ws) > 64:
-                self._ws.clear()
-            self._ws[key] = need
+            with torch.cuda.device(self.device):
+                need = L.mk_attn_workspace_bytes(*key[1:])
+            if len(_scratch) >= 1024:
+                _scratch.clear()
+            _scratch[key] = need
+        return self._on(stream, (q, lens, cu, out, self.k, self.v, self.table), self._launch,
+                        "mk_attn_decode" if decode else "mk_attn_prefill", bt, n, hq, qr,
+                        self.dim ** -0.5 if scale is None else scale, out, given, return_lse, need)
 
-        def call(raw):
-            o, rows = out, given
-            if rows is None:
-                o = torch.empty(q.shape, dtype=_BF16, device=self.device)
-                rows = L.mk_rows(o.data_ptr(), hq * view.head_dim, view.head_dim)
-            lse = torch.empty((n, hq), dtype=torch.float32, device=self.device) \
-                if return_lse else None
-            ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
-            (L.mk_attn_decode if decode else L.mk_attn_prefill)(
-                view, bt, hq, qr, scale, rows, lse.data_ptr() if return_lse else None,
-                ws.data_ptr() if need else None, need, raw)
-            return (o, lse) if return_lse else o
-
-        return self._on(stream, (q, lens, cu, out, self.k, self.v, self.table), call)
+    def _launch(self, raw, name, bt, n, hq, qr, scale, out, rows, return_lse, need):
+        if rows is None:
+            out, rows = self._dense(n, hq)
+        lse = torch.empty((n, hq), dtype=_F32, device=self.device) if return_lse else None
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
+        status = _call(name)(self._view, bt, hq, qr, scale, rows,
+                             lse.data_ptr() if return_lse else None,
+                             ws.data_ptr() if need else None, need, raw)
+        if status:
+            raise L.MkError(status, name)
+        return (out, lse) if return_lse else out
 
     def decode(self, q, lens, *, scale=None, out=None, return_lse=False, stream=None):
         """Attention of one new token per sequence, q [batch][query heads][head_dim]

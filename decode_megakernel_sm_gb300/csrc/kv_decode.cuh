@@ -391,45 +391,89 @@ kv_decode_kernel(const __grid_constant__ AttnArgs a) {
   }
 }
 
-// One block per item: joins the states of the blocks that shared it.
+// One block per (sequence, query head): joins the states of the blocks that
+// shared its item.  What it needs besides the states is found before it waits
+// for the first kernel; then every warp takes every JOIN_WARPS-th state, all
+// loads of four states in flight at once.
+constexpr int JOIN_WARPS = 8;
+
 template <int D, int NT>
-__global__ void __launch_bounds__(D / 2 * 4)
+__global__ void __launch_bounds__(32 * JOIN_WARPS)
 kv_decode_join_kernel(const __grid_constant__ AttnArgs a, int grid) {
   using Sh = DecShape<D, NT>;
-  constexpr int HB = Sh::HB;
-  const int lane = threadIdx.x & 31;
+  constexpr int HB = Sh::HB, E = D / 32, N = 4;
+  __shared__ float so[JOIN_WARPS][D], sm[JOIN_WARPS], sl[JOIN_WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int blocks_of_heads = (a.G + HB - 1) / HB, items = a.kv.Hkv * blocks_of_heads;
-  const int b = blockIdx.x / items, item = blockIdx.x % items;
+  const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
+  const int hb = hq % a.G / HB, head = hq % a.G % HB;
+  const int item = hq / a.G * blocks_of_heads + hb;
   const int units = dec_units(kv_len(a.kv, a.bt, b));
   const long long total = dec_total(a.kv, a.bt, lane) * items;
   const long long first = dec_before(a.kv, a.bt, b, lane) * items + (long long)item * units;
   const int parts = (int)min((long long)grid, total);
   const int i0 = part_of(total, parts, first), i1 = part_of(total, parts, first + units - 1);
+  const int slot0 = part_begin(total, parts, i0) == first ? 0 : 1;
   pdl_wait();
   if (i0 == i1) return;  // that block wrote the result
-  const int head0 = item / blocks_of_heads * a.G + item % blocks_of_heads * HB;
-  const int n_heads = min(HB, a.G - item % blocks_of_heads * HB);
-  const int slot0 = part_begin(total, parts, i0) == first ? 0 : 1;
-  const float* st0 = a.ws + ((size_t)i0 * 2 + slot0) * Sh::STATE;
-  for (int head = threadIdx.x / (D / 2); head < n_heads; head += 4) {
-    const int dim = 2 * (threadIdx.x % (D / 2));
-    float top = -INFINITY, l = 0.f;
-    float2 o = make_float2(0.f, 0.f);
-    for (int i = i0; i <= i1; i++) {
-      const float* st = i == i0 ? st0 : a.ws + (size_t)i * 2 * Sh::STATE;
-      top = fmaxf(top, st[HB * D + head]);
+  float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; e++) o[e] = 0.f;
+  for (int i = i0 + warp; i <= i1; i += N * JOIN_WARPS) {
+    float mi[N], li[N], oi[N][E];
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+      const int j = i + n * JOIN_WARPS;
+      const bool in = j <= i1;
+      const float* st = a.ws + ((size_t)j * 2 + (j == i0 ? slot0 : 0)) * Sh::STATE;
+      mi[n] = in ? st[HB * D + head] : -INFINITY;
+      li[n] = in ? st[HB * D + HB + head] : 0.f;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 y = in ? *(const float2*)(st + head * D + lane * E + e) : make_float2(0.f, 0.f);
+        oi[n][e] = y.x;
+        oi[n][e + 1] = y.y;
+      }
     }
-    for (int i = i0; i <= i1; i++) {
-      const float* st = i == i0 ? st0 : a.ws + (size_t)i * 2 * Sh::STATE;
-      const float f = join_weight(st[HB * D + head], top);
-      const float2 y = *(const float2*)(st + head * D + dim);
-      l = fmaf(st[HB * D + HB + head], f, l);
-      o.x = fmaf(y.x, f, o.x);
-      o.y = fmaf(y.y, f, o.y);
+    float top = m;
+#pragma unroll
+    for (int n = 0; n < N; n++) top = fmaxf(top, mi[n]);
+    const float f = join_weight(m, top);
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < E; e++) o[e] *= f;
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+      const float g = join_weight(mi[n], top);
+      l = fmaf(li[n], g, l);
+#pragma unroll
+      for (int e = 0; e < E; e++) o[e] = fmaf(oi[n][e], g, o[e]);
     }
-    attn_store2(a, b, head0 + head, dim, o.x, o.y, l);
-    if (a.lse && dim == 0) a.lse[(long long)b * a.Hq + head0 + head] = state_lse(top, l);
+    m = top;
   }
+#pragma unroll
+  for (int e = 0; e < E; e++) so[warp][lane * E + e] = o[e];
+  if (lane == 0) {
+    sm[warp] = m;
+    sl[warp] = l;
+  }
+  __syncthreads();
+  const int dim = 2 * threadIdx.x;
+  if (dim >= D) return;
+  float top = -INFINITY;
+  l = 0.f;
+  float2 x = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < JOIN_WARPS; w++) top = fmaxf(top, sm[w]);
+#pragma unroll
+  for (int w = 0; w < JOIN_WARPS; w++) {
+    const float f = join_weight(sm[w], top);
+    l = fmaf(sl[w], f, l);
+    x.x = fmaf(so[w][dim], f, x.x);
+    x.y = fmaf(so[w][dim + 1], f, x.y);
+  }
+  attn_store2(a, b, hq, dim, x.x, x.y, l);
+  if (a.lse && dim == 0) a.lse[(long long)b * a.Hq + hq] = state_lse(top, l);
 }
 
 }  // namespace mk

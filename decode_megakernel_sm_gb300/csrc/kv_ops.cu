@@ -71,10 +71,10 @@ template <int D, int NT>
 static int decode_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
   using Sh = DecShape<D, NT>;
   const int grid = n_sm * Sh::BLOCKS;
-  const long long items = (long long)a.bt.batch * a.kv.Hkv * ((a.G + Sh::HB - 1) / Sh::HB);
-  if (items > 0x7FFFFFFFll) return MK_ERR_UNSUPPORTED;
+  const long long rows = (long long)a.bt.batch * a.Hq;
+  if (rows > 0x7FFFFFFFll) return MK_ERR_UNSUPPORTED;
   kv_decode_kernel<D, NT><<<grid, DEC_THREADS, 0, s>>>(a);
-  if (launch_dependent(kv_decode_join_kernel<D, NT>, (unsigned)items, D / 2 * 4, s, a, grid) !=
+  if (launch_dependent(kv_decode_join_kernel<D, NT>, (unsigned)rows, 32 * JOIN_WARPS, s, a, grid) !=
       cudaSuccess)
     return MK_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
