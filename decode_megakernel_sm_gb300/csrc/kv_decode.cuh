@@ -188,10 +188,10 @@ struct DecWarp {
       float mx = fmaxf(fmaxf(x[0][2 * n], x[0][2 * n + 1]), fmaxf(x[1][2 * n], x[1][2 * n + 1]));
       mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-      if (__any_sync(0xFFFFFFFFu, mx > m[n] + 8.f)) {
-        const float top = fmaxf(m[n], mx);
-        const float f = join_weight(m[n], top);
-        m[n] = top;
+      const bool higher = mx > m[n] + 8.f;
+      if (__any_sync(0xFFFFFFFFu, higher)) {  // (each head by its own scores alone)
+        const float f = higher ? join_weight(m[n], mx) : 1.f;
+        if (higher) m[n] = mx;
         l[n] *= f;
         const float f0 = __shfl_sync(0xFFFFFFFFu, f, 8 * c), f1 = __shfl_sync(0xFFFFFFFFu, f, 8 * c + 4);
 #pragma unroll

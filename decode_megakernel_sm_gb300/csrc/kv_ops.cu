@@ -3,33 +3,13 @@
 #include <cmath>
 
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include "kv_append.cuh"
 #include "kv_decode.cuh"
+#include "kv_prefill.cuh"
 
 namespace mk {
-
-// One warp per (token, query head).
-template <int D>
-__global__ void __launch_bounds__(128) kv_attn_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int t = (int)(w / a.Hq), hq = (int)(w % a.Hq);
-  if (t >= a.bt.n_tokens) return;
-  const int b = kv_seq_of_token(a.bt, t, lane);
-  if (b >= a.bt.batch) return;
-  const int after = a.bt.cu ? __ldg(a.bt.cu + b + 1) - t : 1;
-  const int n = max(0, kv_len(a.kv, a.bt, b) - after + 1);
-  float m, l, o[E];
-  attn_row<D>(a.kv, b, hq / (a.Hq / a.kv.Hkv), (const uint16_t*)a.q.p + t * a.q.ts + hq * a.q.hs,
-              a.scale, 0, n, m, l, o);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint16_t* dst = (uint16_t*)a.o.p + t * a.o.ts + hq * a.o.hs + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e++) dst[e] = to_bf16(l == 0.f ? 0.f : o[e] * inv);
-  if (a.lse && lane == 0) a.lse[(long long)t * a.Hq + hq] = l == 0.f ? -INFINITY : m + logf(l);
-}
 
 // Streaming multiprocessors of the current device, 0 on an error.
 static int sm_count() {
@@ -43,10 +23,10 @@ static int sm_count() {
 // Launch `kernel` so that it may start while the one before it in the stream
 // runs; it waits for that one itself (griddepcontrol.wait).
 template <typename... P>
-static cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block,
+static cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned block,
                                     cudaStream_t s, P... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.stream = s;
   cudaLaunchAttribute at{};
@@ -74,8 +54,60 @@ static int decode_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
   const long long rows = (long long)a.bt.batch * a.Hq;
   if (rows > 0x7FFFFFFFll) return MK_ERR_UNSUPPORTED;
   kv_decode_kernel<D, NT><<<grid, DEC_THREADS, 0, s>>>(a);
-  if (launch_dependent(kv_decode_join_kernel<D, NT>, (unsigned)rows, 32 * JOIN_WARPS, s, a, grid) !=
+  if (launch_dependent(kv_decode_join_kernel<D, NT>, dim3((unsigned)rows), 32 * JOIN_WARPS, s, a, grid) !=
       cudaSuccess)
+    return MK_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+}
+
+// The driver's tensor-map encoder, or nullptr.
+static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
+    PFN_cuTensorMapEncodeTiled_v12000 f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", (void**)&f, 12000,
+                                         cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return f;
+  }();
+  return enc;
+}
+
+// Whether the kernel was compiled to the registers its warps deal out among
+// themselves (fewer would leave them waiting), and may use its shared memory.
+template <int D>
+static bool prefill_ready() {
+  cudaFuncAttributes at{};
+  return cudaFuncGetAttributes(&at, kv_prefill_kernel<D>) == cudaSuccess && at.numRegs == PF_REGS &&
+         cudaFuncSetAttribute(kv_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              PfShape<D>::SMEM) == cudaSuccess;
+}
+
+template <int D>
+static int prefill_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
+  const auto enc = tensor_map_encoder();
+  if (!enc || !prefill_ready<D>()) return MK_ERR_CUDA;
+  const long long rows = (long long)a.kv.n_blocks * a.kv.Hkv * a.kv.block;
+  if (rows >= 0x7FFFFFFFll) return MK_ERR_UNSUPPORTED;
+  PfArgs p{};
+  p.a = a;
+  p.tokens = PF_ROWS / a.G;
+  p.negate = a.scale < 0.f;
+  // (a scale of zero: so small that every finite score rounds to the same weight)
+  p.scale2 = std::fmax(std::fabs(a.scale) * LOG2E, 1e-30f);
+  p.box = a.kv.table && a.kv.block < PF_UNIT ? a.kv.block : PF_UNIT;
+  CUtensorMap maps[2];
+  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)D * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)p.box}, es[2] = {1, 1};
+  for (int i = 0; i < 2; i++)
+    if (enc(&maps[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, (void*)(i == 0 ? a.kv.k : a.kv.v), dims,
+            strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return MK_ERR_CUDA;
+  kv_prefill_kernel<D><<<n_sm, PF_THREADS, PfShape<D>::SMEM, s>>>(p, maps[0], maps[1]);
+  if (n_sm > 1 && launch_dependent(kv_prefill_join_kernel<D>, dim3(n_sm - 1, PF_ROWS / 32), 256, s,
+                                   p, n_sm) != cudaSuccess)
     return MK_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
@@ -177,9 +209,11 @@ extern "C" int mk_attn_workspace_bytes(int decode, int n_tokens, int batch, int 
     return MK_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return MK_ERR_UNSUPPORTED;
   *bytes = 0;
-  if (decode) {
-    const int n = sm_count(), nt = decode_tiles(n_q_heads / n_kv_heads);
-    if (n == 0) return MK_ERR_CUDA;
+  const int n = sm_count(), nt = decode_tiles(n_q_heads / n_kv_heads);
+  if (n == 0) return MK_ERR_CUDA;
+  if (!decode) {
+    *bytes = (head_dim == 64 ? PfShape<64>::STATE : PfShape<128>::STATE) * sizeof(float) * 2 * n;
+  } else {
     *bytes = head_dim == 64 ? (nt == 1 ? decode_ws<64, 1>(n) : decode_ws<64, 2>(n))
                             : (nt == 1 ? decode_ws<128, 1>(n) : decode_ws<128, 2>(n));
   }
@@ -209,20 +243,15 @@ static int attention(bool decode, const mk_kv_view* kv, const mk_kv_batch* bt, i
   a.Hq = n_q_heads;
   a.G = n_q_heads / kv->n_kv_heads;
   a.ws = (float*)d_ws;
-  if (decode) {
-    const int n = sm_count(), nt = decode_tiles(a.G);
-    cudaStream_t s = (cudaStream_t)stream;
-    if (kv->head_dim == 64)
-      return nt == 1 ? decode_launch<64, 1>(a, n, s) : decode_launch<64, 2>(a, n, s);
-    return nt == 1 ? decode_launch<128, 1>(a, n, s) : decode_launch<128, 2>(a, n, s);
-  }
-  const long long warps = (long long)bt->n_tokens * n_q_heads;
-  if (warps > (1ll << 32)) return MK_ERR_UNSUPPORTED;
-  const unsigned grid = (unsigned)((warps + 3) / 4);
+  const int n = sm_count(), nt = decode_tiles(a.G);
   cudaStream_t s = (cudaStream_t)stream;
-  if (kv->head_dim == 64) kv_attn_kernel<64><<<grid, 128, 0, s>>>(a);
-  else kv_attn_kernel<128><<<grid, 128, 0, s>>>(a);
-  return launched();
+  if (!decode) {
+    if (a.G > PF_ROWS / 2) return MK_ERR_UNSUPPORTED;
+    return kv->head_dim == 64 ? prefill_launch<64>(a, n, s) : prefill_launch<128>(a, n, s);
+  }
+  if (kv->head_dim == 64)
+    return nt == 1 ? decode_launch<64, 1>(a, n, s) : decode_launch<64, 2>(a, n, s);
+  return nt == 1 ? decode_launch<128, 1>(a, n, s) : decode_launch<128, 2>(a, n, s);
 }
 
 extern "C" int mk_attn_decode(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q_heads,

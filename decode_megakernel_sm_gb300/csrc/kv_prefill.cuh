@@ -1,0 +1,869 @@
+// kv_prefill.cuh -- causal attention of the new tokens of every sequence over
+// its cache rows, on the fifth-generation tensor cores.
+//
+// Rows and jobs.  The G query heads of a kv head read the same keys, so a row
+// of the matrix product is a (token, head) pair, row = token * G + head, and a
+// job is up to 256 rows (floor(256 / G) whole tokens) of one sequence and kv
+// head: two tiles of 128 rows, the tensor core's M, which share every key and
+// value tile.  A key tile is 128 cache rows (a unit of a job's work).
+//
+// One block per SM runs a piece of the line of all jobs:
+//   warp 0      loads key and value tiles into a ring of stages (tiled TMA, one
+//               box per page piece, 128-byte swizzle)
+//   warp 1      issues the products: S_t = Q_t K^T and O_t += P_t V, both with
+//               the accumulator in tensor memory; P is the A operand straight
+//               from tensor memory, V the transposed (MN-major) B operand
+//   warps 2, 3  load the query tiles (any strides) into swizzled shared memory
+//   warps 4-7   softmax of tile 0, one row per thread: S from tensor memory to
+//   warps 8-11  registers, running maximum and sum in fp32, P (bf16) back to
+//               tensor memory; O's rescale, where a maximum rises by more than
+//               2^8 (rare after the first tiles), and the results.  (tile 1)
+// The two tiles take turns: the tensor cores work on one while the other's
+// softmax runs.  64-dim heads leave tensor memory for P beside S, so that the
+// next S is made while the softmax still works on this one; 128-dim heads fill
+// it (2 x 128 columns S, 2 x 128 O) and P takes S's place.
+//
+// Bound: with 128-dim heads the tensor cores (4 D operations a pair), with
+// 64-dim heads they and the exponentials alike.
+//
+// The line's measure is keys: a job costs its visible rows and PF_JOB_COST for
+// its start and end, and is cut wherever an equal share of the whole ends (or
+// at the job's border where that is near).  Parts of one job end as partial
+// states that a dependent kernel joins.  Everything is found on the device
+// from lens and cu.
+//
+// The weights P are rounded to bf16 (2^-9 of each weight, the accuracy of the
+// output's own rounding); their sum is taken before the rounding.  Cache rows
+// from len on are never part of a product: the tile that holds the end of a
+// sequence takes its values through cp.async with zeros behind the end.  Rows
+// that a query does not see have weight zero, which times an infinite or NaN
+// value of a later token would still be NaN: rows whose result is not finite
+// although their weights are, are redone by attn_row.
+//
+// Every wait is bounded in time; one that runs out sets the status word, and all
+// warps leave through the common end, which frees the tensor memory.
+#pragma once
+#include <cuda.h>
+
+#include "attn_tc.cuh"
+#include "kv_attn.cuh"
+#include "mk_tc.cuh"
+
+namespace mk {
+
+constexpr int PF_THREADS = 384;
+constexpr int PF_REGS = 168;      // per thread at launch (setmaxnreg deals them out anew)
+constexpr int PF_ROWS = 256;      // rows of a job
+constexpr int PF_UNIT = 128;      // cache rows of a unit
+constexpr int PF_JOB_COST = 256;  // a job's start and end, in keys
+constexpr int PF_MIN_SHARE = 4 * PF_UNIT;  // a part of a job is not worth less
+constexpr int PF_SNAP = 16;       // a cut this part of a share from a job's border moves there
+constexpr int PF_AFTER = 1 << 30;
+constexpr unsigned long long PF_TIMEOUT_NS = 2000000000ull;
+
+template <int D>
+struct PfShape {
+  static constexpr bool SEP = D == 64;  // P beside S in tensor memory
+  static constexpr int TILE = 128 * D * 2;
+  static constexpr int STAGES = D == 64 ? 8 : 4;
+  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE;
+  static constexpr uint32_t S_COL = 0, O_COL = 256, P_COL = SEP ? 256 + 2 * D : 0;
+  static constexpr size_t STATE = (size_t)PF_ROWS * (D + 2);  // floats: o [D/4][256][4], m, l [256]
+};
+
+struct PfArgs {
+  AttnArgs a;
+  int tokens;    // per job
+  int negate;    // the scale is negative: scale2 is its magnitude, Q K^T is negated
+  float scale2;  // |scale| log2 e
+  int box;       // rows of a TMA box
+};
+
+// ---- the line of jobs ------------------------------------------------------
+struct PfSeq {
+  int b, len, first, n;  // sequence, its rows, its new tokens' first row and number
+  int jobs;              // of one kv head
+};
+
+struct PfJob {
+  PfSeq s;
+  int h, j;
+};
+
+struct PfCut {
+  PfJob job;
+  int unit;       // 0: before the job; PF_AFTER: behind it; else a cut inside it
+  long long off;  // of the cut from the job's start
+};
+
+MK_DEV PfSeq pf_seq(const PfArgs& p, int b) {
+  PfSeq s{};
+  s.b = b;
+  if (b < p.a.bt.batch) {
+    s.len = kv_len(p.a.kv, p.a.bt, b);
+    kv_new_tokens(p.a.bt, b, s.first, s.n);
+    s.jobs = (s.n + p.tokens - 1) / p.tokens;
+  }
+  return s;
+}
+
+// Keys before job j of one kv head.
+MK_DEV long long pf_before(const PfArgs& p, const PfSeq& s, int j) {
+  const long long base = max(0, s.len - s.n) + PF_JOB_COST;
+  return base * j + (long long)p.tokens * j * (j + 1) / 2;
+}
+
+// Cache rows that the job's token range [.., last] sees, and its units.
+MK_DEV int pf_seen(const PfSeq& s, int token) { return max(0, s.len - s.n + token + 1); }
+MK_DEV int pf_units(const PfArgs& p, const PfJob& w) {
+  return (pf_seen(w.s, min(w.s.n, p.tokens * (w.j + 1)) - 1) + PF_UNIT - 1) / PF_UNIT;
+}
+
+// Length of the line, and the number of parts it is cut into (one warp).
+MK_DEV long long pf_total(const PfArgs& p, int blocks, int lane, int& parts) {
+  long long n = 0, jobs = 0;
+  for (int b = lane; b < p.a.bt.batch; b += 32) {
+    const PfSeq s = pf_seq(p, b);
+    n += pf_before(p, s, s.jobs);
+    jobs += s.jobs;
+  }
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) {
+    n += __shfl_xor_sync(0xFFFFFFFFu, n, w);
+    jobs += __shfl_xor_sync(0xFFFFFFFFu, jobs, w);
+  }
+  n *= p.a.kv.Hkv;
+  jobs *= p.a.kv.Hkv;
+  parts = (int)min((long long)blocks, max(jobs, n / PF_MIN_SHARE));
+  return n;
+}
+
+// Unit of a job at which a cut `off` keys from its start falls.
+MK_DEV int pf_unit_at(const PfArgs& p, const PfJob& w, long long off, long long share) {
+  const int units = pf_units(p, w);
+  const long long size = pf_before(p, w.s, w.j + 1) - pf_before(p, w.s, w.j);
+  if (off <= share / PF_SNAP) return off == 0 || off < size - off ? 0 : PF_AFTER;
+  if (size - off <= share / PF_SNAP) return PF_AFTER;
+  const long long u = (off + PF_UNIT / 2) / PF_UNIT;
+  return u >= units ? PF_AFTER : (int)u;
+}
+
+// Where cut c (keys from the start, below the total) falls (one warp).
+MK_DEV PfCut pf_find(const PfArgs& p, long long c, long long share, int lane) {
+  long long before = 0;
+  PfCut r{};
+  for (int b0 = 0; b0 < p.a.bt.batch; b0 += 32) {
+    const PfSeq s = pf_seq(p, b0 + lane);
+    long long incl = pf_before(p, s, s.jobs) * p.a.kv.Hkv;
+    const long long own = incl;
+#pragma unroll
+    for (int w = 1; w < 32; w <<= 1) {
+      const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, w);
+      if (lane >= w) incl += y;
+    }
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, own > 0 && before + incl > c);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      r.job.s = pf_seq(p, b0 + src);
+      long long rem = c - before - __shfl_sync(0xFFFFFFFFu, incl - own, src);
+      const long long one = pf_before(p, r.job.s, r.job.s.jobs);
+      r.job.h = (int)(rem / one);
+      rem -= one * r.job.h;
+      int lo = 0, hi = r.job.s.jobs - 1;  // the last job that starts at or before rem
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (pf_before(p, r.job.s, mid) <= rem) lo = mid;
+        else hi = mid - 1;
+      }
+      r.job.j = lo;
+      r.off = rem - pf_before(p, r.job.s, lo);
+      r.unit = pf_unit_at(p, r.job, r.off, share);
+      return r;
+    }
+    before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
+  r.job.s.b = p.a.bt.batch;  // the end of the line
+  return r;
+}
+
+MK_DEV void pf_next(const PfArgs& p, PfJob& w) {
+  if (++w.j < w.s.jobs) return;
+  w.j = 0;
+  if (++w.h < p.a.kv.Hkv) return;
+  w.h = 0;
+  do {
+    w.s = pf_seq(p, w.s.b + 1);
+  } while (w.s.b < p.a.bt.batch && w.s.jobs == 0);
+}
+
+MK_DEV bool pf_same(const PfJob& x, const PfJob& y) {
+  return x.s.b == y.s.b && x.h == y.h && x.j == y.j;
+}
+
+// A block's way along its piece of the line: the same for every warp.
+struct PfWalk {
+  PfJob job;
+  PfCut end;
+  int ka, kb;       // units of the present job
+  bool whole;       // all of them
+  bool first;       // the piece's first job
+  bool more;
+
+  MK_DEV void begin(const PfArgs& p, int part, int lane) {
+    int parts;
+    const long long total = pf_total(p, gridDim.x, lane, parts);
+    more = false;
+    if (part >= parts) return;
+    const long long share = total / parts;
+    const PfCut c = pf_find(p, part_begin(total, parts, part), share, lane);
+    end = pf_find(p, part_begin(total, parts, part + 1), share, lane);
+    if (pf_same(c.job, end.job) && c.unit == end.unit) return;
+    job = c.job;
+    ka = c.unit;
+    if (ka == PF_AFTER) {
+      pf_next(p, job);
+      ka = 0;
+    }
+    first = true;
+    more = true;
+    settle(p);
+  }
+  MK_DEV void settle(const PfArgs& p) {
+    if (job.s.b >= p.a.bt.batch || (pf_same(job, end.job) && end.unit == 0)) {
+      more = false;
+      return;
+    }
+    const int units = pf_units(p, job);
+    kb = pf_same(job, end.job) ? min(end.unit, units) : units;
+    whole = ka == 0 && kb == units;
+  }
+  MK_DEV void next(const PfArgs& p) {
+    first = false;
+    if (pf_same(job, end.job)) {
+      more = false;
+      return;
+    }
+    pf_next(p, job);
+    ka = 0;
+    settle(p);
+  }
+  // Rows of tile t, and the end of the units that it takes part in.
+  MK_DEV int rows(const PfArgs& p, int t) const {
+    const int n = min(p.tokens, job.s.n - job.j * p.tokens) * p.a.G;
+    return min(128, n - 128 * t);
+  }
+  MK_DEV int end_of(const PfArgs& p, int t) const {
+    const int n = rows(p, t);
+    if (n <= 0) return ka;
+    const int token = job.j * p.tokens + (128 * t + n - 1) / p.a.G;
+    return max(ka, min(kb, (pf_seen(job.s, token) + PF_UNIT - 1) / PF_UNIT));
+  }
+};
+
+// ---- small pieces ----------------------------------------------------------
+struct PfShared {
+  alignas(8) unsigned long long kv_full[8], kv_empty[8];
+  unsigned long long q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2], o_empty[2];
+  unsigned long long drain;
+  uint32_t tmem;
+  volatile int abort;
+  PfWalk walk[PF_THREADS / 32];  // each warp's own: in registers it would crowd out the work
+};
+
+// Wait for phase `n` (counted from 0) of a barrier; false if the block gave up.
+MK_DEV bool pf_wait(PfShared& sh, const unsigned long long* bar, uint32_t n) {
+  const uint32_t b = smem_u32(bar);
+  if (mbar_try(b, n & 1)) return true;
+  unsigned long long t0 = 0;
+  for (uint32_t it = 1;; it++) {
+    if (mbar_try(b, n & 1)) return true;
+    if ((it & 63) == 0) {
+      if (sh.abort) return false;
+      const unsigned long long t = gtimer();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > PF_TIMEOUT_NS) {
+        sh.abort = 1;
+        kv_fail(MK_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
+// Descriptor of a transposed (MN-major) operand in the 128-byte swizzle: rows
+// of 64 elements along N (128 bytes), 8 rows along K per atom (1024 bytes), the
+// next 64 elements of N at +16384 (leading offset).
+MK_DEV uint64_t sw128_desc_mn(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(16384u >> 4) << 16) |
+         ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
+// D[tmem] (+)= A[tmem] * B, the A operand from tensor memory.
+MK_DEV void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+#define PF_R4(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3])
+#define PF_R16(x, i) PF_R4(x, i), PF_R4(x, i + 4), PF_R4(x, i + 8), PF_R4(x, i + 12)
+#define PF_I4(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3])
+#define PF_I16(x, i) PF_I4(x, i), PF_I4(x, i + 4), PF_I4(x, i + 8), PF_I4(x, i + 12)
+
+// 64 consecutive columns of this thread's tensor-memory lane, and the wait for
+// them in the same statement.
+MK_DEV void tmem_ld64(uint32_t addr, uint32_t* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : PF_R16(x, 0), PF_R16(x, 16), PF_R16(x, 32), PF_R16(x, 48)
+      : "r"(addr)
+      : "memory");
+}
+MK_DEV void tmem_ld32(uint32_t addr, uint32_t* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : PF_R16(x, 0), PF_R16(x, 16)
+      : "r"(addr)
+      : "memory");
+}
+MK_DEV void tmem_st32(uint32_t addr, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31};" ::PF_I16(x, 0),
+      PF_I16(x, 16), "r"(addr)
+      : "memory");
+}
+MK_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+MK_DEV float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// 2^x to about 2 units in the last place; results below 2^-126 are zero.
+MK_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+MK_DEV void cp_async16_zfill(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
+               : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(PF_THREADS, 1)
+kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap) {
+  using Sh = PfShape<D>;
+  constexpr int C = D / 64;  // 64-column halves of a tile
+  constexpr bool SEP = Sh::SEP;
+  extern __shared__ unsigned char raw[];
+  __shared__ PfShared sh;
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  const uint32_t q_smem = base, ring = base + 2 * Sh::TILE;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Sh::STAGES; i++) {
+      mbar_init(smem_u32(&sh.kv_full[i]), 1);
+      mbar_init(smem_u32(&sh.kv_empty[i]), 1);
+    }
+    for (int t = 0; t < 2; t++) {
+      mbar_init(smem_u32(&sh.q_full[t]), 2);
+      mbar_init(smem_u32(&sh.q_empty[t]), 1);
+      mbar_init(smem_u32(&sh.s_full[t]), 1);
+      mbar_init(smem_u32(&sh.s_free[t]), 4);
+      mbar_init(smem_u32(&sh.p_full[t]), 4);
+      mbar_init(smem_u32(&sh.pv_done[t]), 1);
+      mbar_init(smem_u32(&sh.o_empty[t]), 4);
+    }
+    mbar_init(smem_u32(&sh.drain), 1);
+    sh.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), 512);
+  {
+    PfWalk mine;
+    mine.begin(p, blockIdx.x, lane);
+    if (lane == 0) sh.walk[warp] = mine;
+  }
+  const PfWalk& w = sh.walk[warp];
+  // to the warp's next job: by lane 0, the other lanes wait for it
+  auto next_job = [&]() {
+    __syncwarp();
+    if (lane == 0) sh.walk[warp].next(p);
+    __syncwarp();
+  };
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const AttnArgs& a = p.a;
+
+  // The block's registers, PF_REGS x 384, are dealt out anew: 128 x 104 + 256 x 200.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 0) {
+      // ---------------------------------------------------- keys and values ----
+      uint32_t n = 0;  // stages filled so far
+      bool ok = true;
+      const int boxes = PF_UNIT / p.box;
+      for (; w.more && ok; next_job()) {
+        const int ka = w.ka, kb = max(w.end_of(p, 0), w.end_of(p, 1));
+        const int b = w.job.s.b, h = w.job.h, len = w.job.s.len;
+        // the order in which warp 1 takes them
+        const int count = 2 * (kb - ka);
+        for (int i = 0; i < count && ok; i++) {
+          int unit;
+          bool is_v;
+          if (SEP) {  // K0 K1 V0 K2 V1 ..
+            is_v = i == count - 1 || (i > 0 && (i & 1) == 0);
+            unit = ka + (is_v ? (i == count - 1 ? kb - ka - 1 : i / 2 - 1) : (i + 1) / 2);
+          } else {    // K0 V0 K1 V1 ..
+            is_v = i & 1;
+            unit = ka + i / 2;
+          }
+          const int st = n % Sh::STAGES;
+          if (n >= Sh::STAGES) ok = pf_wait(sh, &sh.kv_empty[st], n / Sh::STAGES - 1);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          const uint32_t dst = ring + st * Sh::TILE, bar = smem_u32(&sh.kv_full[st]);
+          const int row = unit * PF_UNIT;
+          if (is_v && row + PF_UNIT > len) {
+            // the end of the sequence: zeros behind it
+            for (int c = lane; c < PF_UNIT * (D / 8); c += 32) {
+              const int r = c / (D / 8), k = c % (D / 8);
+              long long src = -1;
+              if (row + r < len) src = kv_row_of(a.kv, b, h, row + r);
+              cp_async16_zfill(dst + (k >> 3) * 16384 + r * 128 + (((k ^ r) & 7) << 4),
+                               src < 0 ? a.kv.v : a.kv.v + src * D + k * 8, src >= 0);
+            }
+            cp_async_wait_all();
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+          } else {
+            // boxes that hold rows of the sequence (behind its end the keys' scores
+            // are masked, whatever the stage still holds)
+            const int used = min(boxes, (len - row + p.box - 1) / p.box);
+            if (lane == 0) mbar_expect_tx(bar, (uint32_t)used * p.box * D * 2);
+            __syncwarp();
+            if (lane < used) {
+              const int r = row + lane * p.box;
+              long long y = kv_row_of(a.kv, b, h, r);
+              if (y < 0) y = (long long)a.kv.n_blocks * a.kv.Hkv * a.kv.block;  // outside: zeros
+#pragma unroll
+              for (int c = 0; c < C; c++)
+                tma_load_2d(dst + c * 16384 + lane * p.box * 128, is_v ? &vmap : &kmap, 64 * c, (int)y,
+                            bar, policy_evict_normal());
+            }
+          }
+          n++;
+        }
+      }
+      if (!ok) {  // given up: wait for the copies in flight, again with a limit
+        const unsigned long long t0 = gtimer();
+        for (uint32_t i = n > Sh::STAGES ? n - Sh::STAGES : 0; i < n; i++)
+          while (!mbar_try(smem_u32(&sh.kv_full[i % Sh::STAGES]), (i / Sh::STAGES) & 1) &&
+                 gtimer() - t0 < PF_TIMEOUT_NS) {
+          }
+      }
+    } else if (warp == 1) {
+      if (lane == 0) {
+      // --------------------------------------------------------- products ----
+      uint32_t n = 0;              // stages taken
+      uint32_t ns[2] = {0, 0};     // S tiles made
+      uint32_t np[2] = {0, 0};     // P tiles taken
+      uint32_t jobs[2] = {0, 0};
+      const uint32_t id_qk = idesc_bf16(128, 128) | (p.negate ? 1u << 13 : 0u);
+      const uint32_t id_pv = idesc_bf16(128, D) | (1u << 16);
+      bool ok = true;
+      auto stage_wait = [&](uint32_t i) {
+        ok = ok && pf_wait(sh, &sh.kv_full[i % Sh::STAGES], i / Sh::STAGES);
+      };
+      auto qk = [&](int t, uint32_t stage) {
+        if (SEP && ns[t] > 0) ok = ok && pf_wait(sh, &sh.s_free[t], ns[t] - 1);
+        if (!ok) return;
+        tc_fence_after();
+        {
+          const uint32_t kt = ring + (stage % Sh::STAGES) * Sh::TILE, qt = q_smem + t * Sh::TILE;
+#pragma unroll
+          for (int s = 0; s < D / 16; s++)
+            tc_mma_bf16(tmem + Sh::S_COL + 128 * t, sw128_desc(qt + (s >> 2) * 16384 + (s & 3) * 32),
+                        sw128_desc(kt + (s >> 2) * 16384 + (s & 3) * 32), id_qk, s > 0);
+          tc_commit(smem_u32(&sh.s_full[t]));
+        }
+        ns[t]++;
+      };
+      auto pv = [&](int t, uint32_t stage, bool first) {
+        ok = ok && pf_wait(sh, &sh.p_full[t], np[t]);
+        if (first && jobs[t] > 0) ok = ok && pf_wait(sh, &sh.o_empty[t], jobs[t] - 1);
+        if (!ok) return;
+        tc_fence_after();
+        {
+          const uint32_t vt = ring + (stage % Sh::STAGES) * Sh::TILE;
+#pragma unroll
+          for (int s = 0; s < 8; s++)
+            tc_mma_ts(tmem + Sh::O_COL + D * t,
+                      tmem + (SEP ? Sh::P_COL + 64 * t : Sh::S_COL + 128 * t) + 8 * s,
+                      sw128_desc_mn(vt + s * 2048), id_pv, !first || s > 0);
+          tc_commit(smem_u32(&sh.pv_done[t]));
+        }
+        np[t]++;
+      };
+      auto release = [&](uint32_t stage) {
+        if (ok) tc_commit(smem_u32(&sh.kv_empty[stage % Sh::STAGES]));
+      };
+      for (; w.more && ok; sh.walk[1].next(p)) {
+        const int ka = w.ka, e0 = w.end_of(p, 0), e1 = w.end_of(p, 1), kb = max(e0, e1);
+        if (ka == kb) continue;
+        const int e[2] = {e0, e1};
+        stage_wait(n);
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+          if (ka < e[t]) {
+            ok = ok && pf_wait(sh, &sh.q_full[t], jobs[t]);
+            qk(t, n);
+            if (ok && ka + 1 == e[t]) tc_commit(smem_u32(&sh.q_empty[t]));
+          }
+        release(n);
+        n++;
+        for (int j = ka; j < kb && ok; j++) {
+          const bool next = j + 1 < kb;
+          // stages of V(j) and K(j + 1) in the order of their loading
+          const uint32_t sv = n + (SEP && next ? 1 : 0), sk = n + (SEP ? 0 : 1);
+          if (SEP && next) {
+            stage_wait(sk);
+#pragma unroll
+            for (int t = 0; t < 2; t++)
+              if (j + 1 < e[t]) {
+                qk(t, sk);
+                if (ok && j + 2 == e[t]) tc_commit(smem_u32(&sh.q_empty[t]));
+              }
+            release(sk);
+          }
+          stage_wait(sv);
+#pragma unroll
+          for (int t = 0; t < 2; t++) {
+            if (j < e[t]) pv(t, sv, j == ka);
+            if (!SEP && j + 1 < e[t]) {
+              stage_wait(sk);
+              qk(t, sk);
+              if (ok && j + 2 == e[t]) tc_commit(smem_u32(&sh.q_empty[t]));
+            }
+          }
+          release(sv);
+          if (!SEP && next) release(sk);
+          n += next ? 2 : 1;
+        }
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+          if (ka < e[t]) jobs[t]++;
+      }
+      // the products in flight still read shared and write tensor memory
+      tc_commit(smem_u32(&sh.drain));
+      const unsigned long long t0 = gtimer();
+      while (!mbar_try(smem_u32(&sh.drain), 0) && gtimer() - t0 < PF_TIMEOUT_NS) {
+      }
+      }
+    } else {
+      // ------------------------------------------------------------- queries ----
+      uint32_t jobs[2] = {0, 0};
+      bool ok = true;
+      const int i0 = threadIdx.x - 64;
+      for (; w.more && ok; next_job()) {
+        for (int t = 0; t < 2 && ok; t++) {
+          if (w.end_of(p, t) == w.ka) continue;
+          if (jobs[t] > 0) ok = __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.q_empty[t], jobs[t] - 1));
+          if (!ok) break;
+          jobs[t]++;
+          const int rows = w.rows(p, t), token0 = w.job.s.first + w.job.j * p.tokens;
+          const uint32_t dst = q_smem + t * Sh::TILE;
+          const uint16_t* src = (const uint16_t*)a.q.p + (long long)w.job.h * a.G * a.q.hs;
+          for (int c = i0; c < 128 * (D / 8); c += 64) {
+            const int r = c / (D / 8), k = c % (D / 8), row = 128 * t + r;
+            const int token = token0 + row / a.G, g = row % a.G;
+            const bool in = r < rows;
+            cp_async16_zfill(dst + (k >> 3) * 16384 + r * 128 + (((k ^ r) & 7) << 4),
+                             in ? src + token * a.q.ts + g * a.q.hs + k * 8 : src, in);
+          }
+          cp_async_wait_all();
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[t]));
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    // ------------------------------------------------------------- softmax ----
+    const int t = (warp - 4) >> 2;
+    const int r = 32 * (warp & 3) + lane;  // row of the tile
+    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t s_addr = tmem + lane_base + Sh::S_COL + 128 * t;
+    const uint32_t o_addr = tmem + lane_base + Sh::O_COL + D * t;
+    const uint32_t p_addr = SEP ? tmem + lane_base + Sh::P_COL + 64 * t : s_addr;
+    uint32_t n = 0;  // S tiles taken
+    bool ok = true;
+    for (; w.more && ok; next_job()) {
+      const int rows = w.rows(p, t);
+      if (rows <= 0) continue;
+      const int ka = w.ka, kb = w.end_of(p, t);
+      const int row = 128 * t + r, token = w.job.j * p.tokens + row / a.G;
+      // the last cache row this row sees (rows that do not exist: every one)
+      const int last = r < rows ? w.job.s.len - w.job.s.n + token : 0x3FFFFFFF;
+      float m = -INFINITY, l = 0.f;
+      for (int j = ka; j < kb; j++) {
+        ok = __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.s_full[t], n));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t x[128];
+        tmem_ld64(s_addr, x);
+        tmem_ld64(s_addr + 64, x + 64);
+        if (SEP) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.s_free[t]));
+        }
+        const int limit = last - j * PF_UNIT;  // columns 0 .. limit count
+        if (__any_sync(0xFFFFFFFFu, limit < PF_UNIT - 1)) {
+#pragma unroll
+          for (int i = 0; i < 128; i++)
+            if (i > limit) x[i] = 0xFF800000u;  // -inf
+        }
+        float mx0 = __uint_as_float(x[0]), mx1 = __uint_as_float(x[1]);
+#pragma unroll
+        for (int i = 2; i < 126; i += 4) {
+          mx0 = max3(mx0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+          mx1 = max3(mx1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+        }
+        const float mx = max3(fmaxf(mx0, mx1), __uint_as_float(x[126]), __uint_as_float(x[127])) * p.scale2;
+        // O and P are this thread's to write once the product before is done
+        const bool higher = mx > m + 8.f, raise = __any_sync(0xFFFFFFFFu, higher);
+        if (j > ka && (SEP || raise)) {
+          ok = __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.pv_done[t], n - 1));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        if (raise) {
+          // (each row by its own scores alone, so that no row's bits depend on another)
+          const float f = higher ? join_weight(m, mx) : 1.f;
+          if (higher) m = mx;
+          l *= f;
+          if (j > ka) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t y[32];
+              tmem_ld32(o_addr + c, y);
+#pragma unroll
+              for (int i = 0; i < 32; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+              tmem_st32(o_addr + c, y);
+            }
+          }
+        }
+        const float neg = m == -INFINITY ? 0.f : -m;
+        const float2 sc = make_float2(p.scale2, p.scale2), ng = make_float2(neg, neg);
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+          uint32_t y[32];
+#pragma unroll
+          for (int i = 0; i < 32; i++) {
+            const int k = 64 * half + 2 * i;
+            float2 e = ffma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), sc, ng);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            sum = fadd2(sum, e);
+            y[i] = bf2(e.x, e.y);
+          }
+          tmem_st32(p_addr + 32 * half, y);
+        }
+        l += sum.x + sum.y;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[t]));
+        n++;
+      }
+      if (!ok) break;
+      // -- the job's end: out = o / l, or a partial state
+      if (kb > ka) {
+        ok = __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.pv_done[t], n - 1));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const bool mine = r < rows;
+      const int hq = w.job.h * a.G + row % a.G;
+      const long long tok = w.job.s.first + token;
+      float* st = a.ws + ((size_t)blockIdx.x * 2 + (w.first ? 0 : 1)) * Sh::STATE;
+      uint16_t* out = (uint16_t*)a.o.p + tok * a.o.ts + hq * a.o.hs;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      float bad = 0.f;
+      if (kb > ka) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t y[32];
+          tmem_ld32(o_addr + c, y);
+#pragma unroll
+          for (int i = 0; i < 32; i++) bad = fmaf(__uint_as_float(y[i]), 0.f, bad);
+          if (mine && w.whole) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              float f[8];
+#pragma unroll
+              for (int e = 0; e < 8; e++) f[e] = l == 0.f ? 0.f : __uint_as_float(y[i + e]) * inv;
+              *(uint4*)(out + c + i) = make_uint4(bf2(f[0], f[1]), bf2(f[2], f[3]), bf2(f[4], f[5]),
+                                                  bf2(f[6], f[7]));
+            }
+          } else if (mine) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *(uint4*)(st + ((size_t)(c + i) / 4 * PF_ROWS + row) * 4) =
+                  make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.o_empty[t]));
+      } else if (mine && w.whole) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 8) *(uint4*)(out + c) = make_uint4(0, 0, 0, 0);
+      }
+      if (mine) {
+        if (w.whole) {
+          if (a.lse) a.lse[tok * a.Hq + hq] = state_lse(m, l);
+        } else {
+          st[PF_ROWS * D + row] = m;
+          st[PF_ROWS * D + PF_ROWS + row] = l;
+        }
+      }
+      __syncwarp();
+      unsigned redo = __ballot_sync(0xFFFFFFFFu, mine && !(bad == 0.f) && isfinite(l));
+      while (redo) {
+        const int src = __ffs(redo) - 1;
+        redo &= redo - 1;
+        const int rr = __shfl_sync(0xFFFFFFFFu, row, src);
+        const int end = __shfl_sync(0xFFFFFFFFu, last, src) + 1;
+        const int tk = w.job.j * p.tokens + rr / a.G;
+        const int hh = w.job.h * a.G + rr % a.G;
+        const long long row_tok = w.job.s.first + tk;
+        float m1, l1, o1[D / 32];
+        attn_row<D>(a.kv, w.job.s.b, w.job.h, (const uint16_t*)a.q.p + row_tok * a.q.ts + hh * a.q.hs,
+                    a.scale, ka * PF_UNIT, min(end, kb * PF_UNIT), m1, l1, o1);
+        // a partial state keeps the row's m and l, which are sound
+        const float f1 = w.whole ? (l1 == 0.f ? 0.f : 1.f / l1)
+                                 : join_weight(m1 * LOG2E, __shfl_sync(0xFFFFFFFFu, m, src));
+#pragma unroll
+        for (int e = 0; e < D / 32; e++) {
+          const int dim = lane * (D / 32) + e;
+          if (w.whole)
+            ((uint16_t*)a.o.p)[row_tok * a.o.ts + hh * a.o.hs + dim] = to_bf16(o1[e] * f1);
+          else
+            st[((size_t)(dim / 4) * PF_ROWS + rr) * 4 + dim % 4] = o1[e] * f1;
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Block (x, y): if cut x + 1 of the line is the first inside its job, joins rows
+// [32 y, 32 y + 32) of that job's parts.  A warp has 32 rows, one per lane, and
+// an eighth of the head's dimensions.
+template <int D>
+__global__ void __launch_bounds__(256) kv_prefill_join_kernel(const __grid_constant__ PfArgs p, int blocks) {
+  using Sh = PfShape<D>;
+  constexpr int N = D / 32;  // float4 pieces per warp
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i = blockIdx.x + 1;
+  const AttnArgs& a = p.a;
+  int parts;
+  const long long total = pf_total(p, blocks, lane, parts);
+  bool mine = i < parts;
+  PfCut cut{};
+  int slot = 0;
+  const long long share = total / max(parts, 1);
+  if (mine) {
+    cut = pf_find(p, part_begin(total, parts, i), share, lane);
+    const PfCut prev = pf_find(p, part_begin(total, parts, i - 1), share, lane);
+    const bool inside = cut.unit > 0 && cut.unit < PF_AFTER;
+    const bool same = pf_same(prev.job, cut.job);
+    mine = inside && !(same && prev.unit > 0 && prev.unit < PF_AFTER);
+    if (mine) {  // slot 0: the job is the first one of block i - 1
+      PfJob start = prev.job;
+      if (prev.unit == PF_AFTER) pf_next(p, start);
+      const bool whole_start = prev.unit == PF_AFTER || prev.unit == 0;
+      slot = whole_start && pf_same(start, cut.job) ? 0 : 1;
+    }
+  }
+  pdl_wait();
+  if (!mine) return;
+  const int row = 32 * blockIdx.y + lane;
+  const int n_rows = min(p.tokens, cut.job.s.n - cut.job.j * p.tokens) * a.G;
+  const bool live = row < n_rows;
+  const long long start = part_begin(total, parts, i) - cut.off;  // of the job on the line
+  float m = -INFINITY, l = 0.f;
+  float4 o[N];
+#pragma unroll
+  for (int c = 0; c < N; c++) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  int unit = 0;  // where the part begins
+  for (int k = i - 1;; k++) {
+    // part k ends at cut k + 1
+    const int next = k + 1 >= parts ? PF_AFTER
+                                    : pf_unit_at(p, cut.job, part_begin(total, parts, k + 1) - start, share);
+    const bool beyond = k + 1 >= parts ||
+        part_begin(total, parts, k + 1) - start >= pf_before(p, cut.job.s, cut.job.j + 1) - pf_before(p, cut.job.s, cut.job.j);
+    const int until = beyond ? PF_AFTER : next;
+    if (until > unit && live) {
+      const float* st = a.ws + ((size_t)k * 2 + (k == i - 1 ? slot : 0)) * Sh::STATE;
+      const float mi = st[PF_ROWS * D + row], li = st[PF_ROWS * D + PF_ROWS + row];
+      if (!(li == 0.f)) {
+        const float top = fmaxf(m, mi), f = join_weight(m, top), g = join_weight(mi, top);
+        m = top;
+        l = l * f + li * g;
+#pragma unroll
+        for (int c = 0; c < N; c++) {
+          const float4 y = *(const float4*)(st + ((size_t)(warp * N + c) * PF_ROWS + row) * 4);
+          o[c].x = o[c].x * f + y.x * g;
+          o[c].y = o[c].y * f + y.y * g;
+          o[c].z = o[c].z * f + y.z * g;
+          o[c].w = o[c].w * f + y.w * g;
+        }
+      }
+    }
+    if (until == PF_AFTER) break;
+    unit = until;
+  }
+  if (!live) return;
+  const int token = cut.job.j * p.tokens + row / a.G, hq = cut.job.h * a.G + row % a.G;
+  const long long tok = cut.job.s.first + token;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint16_t* out = (uint16_t*)a.o.p + tok * a.o.ts + hq * a.o.hs + warp * N * 4;
+#pragma unroll
+  for (int c = 0; c < N; c++)
+    *(uint2*)(out + 4 * c) = l == 0.f ? make_uint2(0, 0)
+                                      : make_uint2(bf2(o[c].x * inv, o[c].y * inv),
+                                                   bf2(o[c].z * inv, o[c].w * inv));
+  if (a.lse && warp == 0) a.lse[tok * a.Hq + hq] = state_lse(m, l);
+}
+
+}  // namespace mk
