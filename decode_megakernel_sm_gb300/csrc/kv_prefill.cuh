@@ -8,16 +8,19 @@
 // value tile.  A key tile is 128 cache rows (a unit of a job's work).
 //
 // One block per SM runs a piece of the line of all jobs:
-//   warp 0      loads key and value tiles into a ring of stages (tiled TMA, one
-//               box per page piece, 128-byte swizzle)
+//   warps 0, 2  load key tiles (0) and value tiles (2) into rings of stages
+//               (tiled TMA, one box per page piece, 128-byte swizzle)
 //   warp 1      issues the products: S_t = Q_t K^T and O_t += P_t V, both with
 //               the accumulator in tensor memory; P is the A operand straight
 //               from tensor memory, V the transposed (MN-major) B operand
-//   warps 2, 3  load the query tiles (any strides) into swizzled shared memory
-//   warps 4-7   softmax of tile 0, one row per thread: S from tensor memory to
-//   warps 8-11  registers, running maximum and sum in fp32, P (bf16) back to
-//               tensor memory; O's rescale, where a maximum rises by more than
-//               2^8 (rare after the first tiles), and the results.  (tile 1)
+//   warp 3      walks the block's piece of the line and posts one record per job
+//               in a ring, so that the others do no arithmetic on jobs
+//   warps 4-7   softmax of tile 0, one row per thread: the row's queries into
+//               shared memory, S from tensor memory to registers, running maximum
+//               and sum in fp32, P (bf16) back to tensor memory; O's rescale,
+//               where a maximum rises by more than 2^8 (rare after the first
+//               tiles), and the results
+//   warps 8-11  the same for tile 1
 // The two tiles take turns: the tensor cores work on one while the other's
 // softmax runs.  64-dim heads leave tensor memory for P beside S, so that the
 // next S is made while the softmax still works on this one; 128-dim heads fill
@@ -65,8 +68,8 @@ template <int D>
 struct PfShape {
   static constexpr bool SEP = D == 64;  // P beside S in tensor memory
   static constexpr int TILE = 128 * D * 2;
-  static constexpr int STAGES = D == 64 ? 8 : 4;
-  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE;
+  static constexpr int STAGES = D == 64 ? 4 : 2;  // of keys, and as many of values
+  static constexpr int SMEM = 1024 + 2 * TILE + 2 * STAGES * TILE;
   static constexpr uint32_t S_COL = 0, O_COL = 256, P_COL = SEP ? 256 + 2 * D : 0;
   static constexpr size_t STATE = (size_t)PF_ROWS * (D + 2);  // floats: o [D/4][256][4], m, l [256]
 };
@@ -119,11 +122,20 @@ MK_DEV int pf_units(const PfArgs& p, const PfJob& w) {
   return (pf_seen(w.s, min(w.s.n, p.tokens * (w.j + 1)) - 1) + PF_UNIT - 1) / PF_UNIT;
 }
 
-// Length of the line, and the number of parts it is cut into (one warp).
-MK_DEV long long pf_total(const PfArgs& p, int blocks, int lane, int& parts) {
-  long long n = 0, jobs = 0;
+// How the line is cut: part i begins at quot * i + rest * i / parts.
+struct PfLine {
+  long long total, quot;
+  int parts, rest;
+  long long snap;  // a cut this near to a job's border moves there
+  MK_DEV long long begin(int i) const { return quot * i + (unsigned)rest * (unsigned)i / (unsigned)parts; }
+};
+
+// The whole line (one warp; s0: this lane's sequence among the first 32).
+MK_DEV PfLine pf_line(const PfArgs& p, int blocks, int lane, const PfSeq& s0) {
+  long long n = 0;
+  int jobs = 0;
   for (int b = lane; b < p.a.bt.batch; b += 32) {
-    const PfSeq s = pf_seq(p, b);
+    const PfSeq s = b < 32 ? s0 : pf_seq(p, b);
     n += pf_before(p, s, s.jobs);
     jobs += s.jobs;
   }
@@ -132,57 +144,97 @@ MK_DEV long long pf_total(const PfArgs& p, int blocks, int lane, int& parts) {
     n += __shfl_xor_sync(0xFFFFFFFFu, n, w);
     jobs += __shfl_xor_sync(0xFFFFFFFFu, jobs, w);
   }
-  n *= p.a.kv.Hkv;
-  jobs *= p.a.kv.Hkv;
-  parts = (int)min((long long)blocks, max(jobs, n / PF_MIN_SHARE));
-  return n;
+  PfLine l;
+  l.total = n * p.a.kv.Hkv;
+  l.parts = (int)min((long long)blocks, max((long long)jobs * p.a.kv.Hkv, l.total / PF_MIN_SHARE));
+  if (l.parts > 0) {
+    l.quot = l.total / l.parts;
+    l.rest = (int)(l.total - l.quot * l.parts);
+    l.snap = l.quot / PF_SNAP;
+  }
+  return l;
 }
 
 // Unit of a job at which a cut `off` keys from its start falls.
-MK_DEV int pf_unit_at(const PfArgs& p, const PfJob& w, long long off, long long share) {
+MK_DEV int pf_unit_at(const PfArgs& p, const PfJob& w, long long off, long long snap) {
   const int units = pf_units(p, w);
   const long long size = pf_before(p, w.s, w.j + 1) - pf_before(p, w.s, w.j);
-  if (off <= share / PF_SNAP) return off == 0 || off < size - off ? 0 : PF_AFTER;
-  if (size - off <= share / PF_SNAP) return PF_AFTER;
+  if (off <= snap) return off == 0 || off < size - off ? 0 : PF_AFTER;
+  if (size - off <= snap) return PF_AFTER;
   const long long u = (off + PF_UNIT / 2) / PF_UNIT;
   return u >= units ? PF_AFTER : (int)u;
 }
 
-// Where cut c (keys from the start, below the total) falls (one warp).
-MK_DEV PfCut pf_find(const PfArgs& p, long long c, long long share, int lane) {
+// Where cut c (keys from the start) falls; from the total on, the end of the
+// line (one warp, c the same or not on its lanes as `c0` for the even and `c1`
+// for the odd ones: two cuts for the price of one).
+MK_DEV PfCut pf_find(const PfArgs& p, long long c0, long long c1, long long snap, int lane, const PfSeq& s0) {
   long long before = 0;
   PfCut r{};
+  r.job.s.b = p.a.bt.batch;
+  const long long c = lane & 1 ? c1 : c0;
+  long long rem = -1;
   for (int b0 = 0; b0 < p.a.bt.batch; b0 += 32) {
-    const PfSeq s = pf_seq(p, b0 + lane);
-    long long incl = pf_before(p, s, s.jobs) * p.a.kv.Hkv;
-    const long long own = incl;
+    const PfSeq s = b0 == 0 ? s0 : pf_seq(p, b0 + lane);
+    const long long own = pf_before(p, s, s.jobs) * p.a.kv.Hkv;
+    long long incl = own;
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
       const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, w);
       if (lane >= w) incl += y;
     }
-    const unsigned hit = __ballot_sync(0xFFFFFFFFu, own > 0 && before + incl > c);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      r.job.s = pf_seq(p, b0 + src);
-      long long rem = c - before - __shfl_sync(0xFFFFFFFFu, incl - own, src);
-      const long long one = pf_before(p, r.job.s, r.job.s.jobs);
-      r.job.h = (int)(rem / one);
-      rem -= one * r.job.h;
-      int lo = 0, hi = r.job.s.jobs - 1;  // the last job that starts at or before rem
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (pf_before(p, r.job.s, mid) <= rem) lo = mid;
-        else hi = mid - 1;
-      }
-      r.job.j = lo;
-      r.off = rem - pf_before(p, r.job.s, lo);
-      r.unit = pf_unit_at(p, r.job, r.off, share);
-      return r;
+    const unsigned hit0 = __ballot_sync(0xFFFFFFFFu, own > 0 && before + incl > c0);
+    const unsigned hit1 = __ballot_sync(0xFFFFFFFFu, own > 0 && before + incl > c1);
+    const unsigned hit = lane & 1 ? hit1 : hit0;
+    const int src = hit ? __ffs(hit) - 1 : 0;
+    PfSeq t;
+    t.b = b0 + src;
+    t.len = __shfl_sync(0xFFFFFFFFu, s.len, src);
+    t.first = __shfl_sync(0xFFFFFFFFu, s.first, src);
+    t.n = __shfl_sync(0xFFFFFFFFu, s.n, src);
+    t.jobs = __shfl_sync(0xFFFFFFFFu, s.jobs, src);
+    const long long start = before + __shfl_sync(0xFFFFFFFFu, incl - own, src);
+    if (hit && rem < 0) {
+      r.job.s = t;
+      rem = c - start;
     }
+    if (hit0 && hit1) break;
     before += __shfl_sync(0xFFFFFFFFu, incl, 31);
   }
-  r.job.s.b = p.a.bt.batch;  // the end of the line
+  if (rem >= 0) {
+    // kv head, then the last job that starts at or before rem: estimates in
+    // floating point, put right in whole numbers
+    const PfSeq& q = r.job.s;
+    const long long one = pf_before(p, q, q.jobs);
+    int h = min((int)((float)rem / (float)one), p.a.kv.Hkv - 1);
+    while (h > 0 && one * h > rem) h--;
+    while (one * (h + 1) <= rem) h++;
+    rem -= one * h;
+    r.job.h = h;
+    const float base = (float)(max(0, q.len - q.n) + PF_JOB_COST) + 0.5f * p.tokens;
+    int j = (int)((sqrtf(base * base + 2.f * p.tokens * (float)rem) - base) / p.tokens);
+    j = min(max(j, 0), q.jobs - 1);
+    while (j > 0 && pf_before(p, q, j) > rem) j--;
+    while (j + 1 < q.jobs && pf_before(p, q, j + 1) <= rem) j++;
+    r.job.j = j;
+    r.off = rem - pf_before(p, q, j);
+    r.unit = pf_unit_at(p, r.job, r.off, snap);
+  }
+  return r;
+}
+
+// The cut that lane `src` found.
+MK_DEV PfCut pf_shfl(const PfCut& c, int src) {
+  PfCut r;
+  r.job.s.b = __shfl_sync(0xFFFFFFFFu, c.job.s.b, src);
+  r.job.s.len = __shfl_sync(0xFFFFFFFFu, c.job.s.len, src);
+  r.job.s.first = __shfl_sync(0xFFFFFFFFu, c.job.s.first, src);
+  r.job.s.n = __shfl_sync(0xFFFFFFFFu, c.job.s.n, src);
+  r.job.s.jobs = __shfl_sync(0xFFFFFFFFu, c.job.s.jobs, src);
+  r.job.h = __shfl_sync(0xFFFFFFFFu, c.job.h, src);
+  r.job.j = __shfl_sync(0xFFFFFFFFu, c.job.j, src);
+  r.unit = __shfl_sync(0xFFFFFFFFu, c.unit, src);
+  r.off = __shfl_sync(0xFFFFFFFFu, c.off, src);
   return r;
 }
 
@@ -200,7 +252,7 @@ MK_DEV bool pf_same(const PfJob& x, const PfJob& y) {
   return x.s.b == y.s.b && x.h == y.h && x.j == y.j;
 }
 
-// A block's way along its piece of the line: the same for every warp.
+// A block's way along its piece of the line.
 struct PfWalk {
   PfJob job;
   PfCut end;
@@ -210,13 +262,13 @@ struct PfWalk {
   bool more;
 
   MK_DEV void begin(const PfArgs& p, int part, int lane) {
-    int parts;
-    const long long total = pf_total(p, gridDim.x, lane, parts);
+    const PfSeq s0 = pf_seq(p, lane);
+    const PfLine line = pf_line(p, gridDim.x, lane, s0);
     more = false;
-    if (part >= parts) return;
-    const long long share = total / parts;
-    const PfCut c = pf_find(p, part_begin(total, parts, part), share, lane);
-    end = pf_find(p, part_begin(total, parts, part + 1), share, lane);
+    if (part >= line.parts) return;
+    const PfCut both = pf_find(p, line.begin(part), line.begin(part + 1), line.snap, lane, s0);
+    const PfCut c = pf_shfl(both, 0);
+    end = pf_shfl(both, 1);
     if (pf_same(c.job, end.job) && c.unit == end.unit) return;
     job = c.job;
     ka = c.unit;
@@ -261,13 +313,26 @@ struct PfWalk {
 };
 
 // ---- small pieces ----------------------------------------------------------
+// What the roles need to know about a job, and how they pass it on.
+struct PfRec {
+  int b, h, len;        // sequence, kv head, cache rows (b < 0: no more jobs)
+  int row, pos;         // first token of the job: its row of q, its position
+  int ka, e[2];         // units [ka, e[t]) for tile t
+  int rows[2];          // rows of tile t (none: <= 0)
+  int whole, slot;      // all units of the job; slot of its partial state
+};
+
+constexpr int PF_RECS = 4;
+constexpr int PF_READERS = 11;  // warps that read the records (all but warp 3)
+
 struct PfShared {
-  alignas(8) unsigned long long kv_full[8], kv_empty[8];
-  unsigned long long q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2], o_empty[2];
+  alignas(8) unsigned long long k_full[4], k_empty[4], v_full[4], v_empty[4];
+  unsigned long long rec_full[PF_RECS], rec_empty[PF_RECS];
+  unsigned long long q_full[2], s_full[2], s_free[2], p_full[2], pv_done[2], o_empty[2];
   unsigned long long drain;
+  PfRec rec[PF_RECS];
   uint32_t tmem;
   volatile int abort;
-  PfWalk walk[PF_THREADS / 32];  // each warp's own: in registers it would crowd out the work
 };
 
 // Wait for phase `n` (counted from 0) of a barrier; false if the block gave up.
@@ -290,21 +355,48 @@ MK_DEV bool pf_wait(PfShared& sh, const unsigned long long* bar, uint32_t n) {
   }
 }
 
-// Descriptor of a transposed (MN-major) operand in the 128-byte swizzle: rows
-// of 64 elements along N (128 bytes), 8 rows along K per atom (1024 bytes), the
-// next 64 elements of N at +16384 (leading offset).
-MK_DEV uint64_t sw128_desc_mn(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(16384u >> 4) << 16) |
-         ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+// The next record (one warp): false if the block gave up or there are no more jobs.
+MK_DEV bool pf_take(PfShared& sh, uint32_t& n, PfRec& r, bool lead) {
+  const int i = n % PF_RECS;
+  if (!__all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.rec_full[i], n / PF_RECS))) return false;
+  r = sh.rec[i];
+  __syncwarp();
+  if (lead) mbar_arrive(smem_u32(&sh.rec_empty[i]));
+  n++;
+  return r.b >= 0;
 }
 
-// D[tmem] (+)= A[tmem] * B, the A operand from tensor memory.
-MK_DEV void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, bool accumulate) {
+// Low and high words of shared-memory matrix descriptors in the 128-byte
+// swizzle (the fields are those of sw128_desc): 8-row atoms 1024 bytes apart.
+// For a transposed (MN-major) operand a row holds 64 elements along N, an atom 8
+// rows along K, and the next 64 elements of N follow at +16384 (the leading offset).
+constexpr uint32_t DESC_HI = 0x40004040u;
+MK_DEV uint32_t desc_lo(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
+MK_DEV uint32_t desc_lo_mn(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | ((16384u >> 4) << 16); }
+
+// D[tmem] (+)= A * B^T, both operands from shared memory.
+MK_DEV void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n mov.b64 a, {%1, %5};\n mov.b64 b, {%2, %5};\n"
+      " setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "n"(DESC_HI)
       : "memory");
+}
+
+// The same with the A operand from tensor memory.
+MK_DEV void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 b;\n mov.b64 b, {%2, %5};\n"
+      " setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "n"(DESC_HI)
+      : "memory");
+}
+
+// True on one lane of the (whole) warp.
+MK_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
 }
 
 #define PF_R4(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3])
@@ -370,21 +462,27 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
   using Sh = PfShape<D>;
   constexpr int C = D / 64;  // 64-column halves of a tile
   constexpr bool SEP = Sh::SEP;
+  constexpr uint32_t NS = Sh::STAGES;
   extern __shared__ unsigned char raw[];
   __shared__ PfShared sh;
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-  const uint32_t q_smem = base, ring = base + 2 * Sh::TILE;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t q_smem = base, k_ring = base + 2 * Sh::TILE, v_ring = k_ring + NS * Sh::TILE;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   pdl_launch_dependents();
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Sh::STAGES; i++) {
-      mbar_init(smem_u32(&sh.kv_full[i]), 1);
-      mbar_init(smem_u32(&sh.kv_empty[i]), 1);
+    for (int i = 0; i < NS; i++) {
+      mbar_init(smem_u32(&sh.k_full[i]), 1);
+      mbar_init(smem_u32(&sh.k_empty[i]), 1);
+      mbar_init(smem_u32(&sh.v_full[i]), 1);
+      mbar_init(smem_u32(&sh.v_empty[i]), 1);
+    }
+    for (int i = 0; i < PF_RECS; i++) {
+      mbar_init(smem_u32(&sh.rec_full[i]), 1);
+      mbar_init(smem_u32(&sh.rec_empty[i]), PF_READERS);
     }
     for (int t = 0; t < 2; t++) {
-      mbar_init(smem_u32(&sh.q_full[t]), 2);
-      mbar_init(smem_u32(&sh.q_empty[t]), 1);
+      mbar_init(smem_u32(&sh.q_full[t]), 4);
       mbar_init(smem_u32(&sh.s_full[t]), 1);
       mbar_init(smem_u32(&sh.s_free[t]), 4);
       mbar_init(smem_u32(&sh.p_full[t]), 4);
@@ -396,18 +494,6 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), 512);
-  {
-    PfWalk mine;
-    mine.begin(p, blockIdx.x, lane);
-    if (lane == 0) sh.walk[warp] = mine;
-  }
-  const PfWalk& w = sh.walk[warp];
-  // to the warp's next job: by lane 0, the other lanes wait for it
-  auto next_job = [&]() {
-    __syncwarp();
-    if (lane == 0) sh.walk[warp].next(p);
-    __syncwarp();
-  };
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -417,38 +503,44 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
   // The block's registers, PF_REGS x 384, are dealt out anew: 128 x 104 + 256 x 200.
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    if (warp == 0) {
-      // ---------------------------------------------------- keys and values ----
-      uint32_t n = 0;  // stages filled so far
+    if (warp == 0 || warp == 2) {
+      // ------------------------------------- keys (warp 0), values (warp 2) ----
+      const bool is_v = warp == 2;
+      const uint32_t ring = is_v ? v_ring : k_ring;
+      unsigned long long* full = is_v ? sh.v_full : sh.k_full;
+      const unsigned long long* empty = is_v ? sh.v_empty : sh.k_empty;
+      const void* map = is_v ? &vmap : &kmap;
+      const uint64_t policy = policy_evict_normal();
+      const int shift = a.kv.shift, in_block = a.kv.table ? a.kv.block - 1 : 0x7FFFFFFF;
+      const uint32_t my_box = (uint32_t)lane * p.box;
+      uint32_t n = 0, taken = 0;  // stages filled, records taken
       bool ok = true;
-      const int boxes = PF_UNIT / p.box;
-      for (; w.more && ok; next_job()) {
-        const int ka = w.ka, kb = max(w.end_of(p, 0), w.end_of(p, 1));
-        const int b = w.job.s.b, h = w.job.h, len = w.job.s.len;
-        // the order in which warp 1 takes them
-        const int count = 2 * (kb - ka);
-        for (int i = 0; i < count && ok; i++) {
-          int unit;
-          bool is_v;
-          if (SEP) {  // K0 K1 V0 K2 V1 ..
-            is_v = i == count - 1 || (i > 0 && (i & 1) == 0);
-            unit = ka + (is_v ? (i == count - 1 ? kb - ka - 1 : i / 2 - 1) : (i + 1) / 2);
-          } else {    // K0 V0 K1 V1 ..
-            is_v = i & 1;
-            unit = ka + i / 2;
-          }
-          const int st = n % Sh::STAGES;
-          if (n >= Sh::STAGES) ok = pf_wait(sh, &sh.kv_empty[st], n / Sh::STAGES - 1);
-          ok = __all_sync(0xFFFFFFFFu, ok);
+      PfRec w;
+      while (ok && pf_take(sh, taken, w, lane == 0)) {
+        const int kb = max(w.e[0], w.e[1]);
+        if (kb == w.ka) continue;
+        // Block of this lane's box of a unit, looked up one unit ahead; a lane
+        // whose box begins behind the sequence's end has none to load.
+        const int* table = a.kv.table + (size_t)w.b * a.kv.table_stride;
+        auto lookup = [&](int unit) {
+          const int r = min(unit * PF_UNIT + (int)my_box, w.len - 1);
+          return a.kv.table ? __ldg(table + (r >> shift)) : w.b;
+        };
+        int ahead = lookup(w.ka);
+        for (int j = w.ka; j < kb; j++) {
+          const int blk = ahead;
+          if (j + 1 < kb) ahead = lookup(j + 1);
+          const uint32_t st = n % NS, dst = ring + st * Sh::TILE, bar = smem_u32(&full[st]);
+          if (n >= NS) ok = __all_sync(0xFFFFFFFFu, pf_wait(sh, &empty[st], n / NS - 1));
           if (!ok) break;
-          const uint32_t dst = ring + st * Sh::TILE, bar = smem_u32(&sh.kv_full[st]);
-          const int row = unit * PF_UNIT;
-          if (is_v && row + PF_UNIT > len) {
+          n++;
+          const int row = j * PF_UNIT, left = w.len - row;
+          if (is_v && left < PF_UNIT) {
             // the end of the sequence: zeros behind it
             for (int c = lane; c < PF_UNIT * (D / 8); c += 32) {
               const int r = c / (D / 8), k = c % (D / 8);
               long long src = -1;
-              if (row + r < len) src = kv_row_of(a.kv, b, h, row + r);
+              if (r < left) src = kv_row_of(a.kv, w.b, w.h, row + r);
               cp_async16_zfill(dst + (k >> 3) * 16384 + r * 128 + (((k ^ r) & 7) << 4),
                                src < 0 ? a.kv.v : a.kv.v + src * D + k * 8, src >= 0);
             }
@@ -459,153 +551,158 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
           } else {
             // boxes that hold rows of the sequence (behind its end the keys' scores
             // are masked, whatever the stage still holds)
-            const int used = min(boxes, (len - row + p.box - 1) / p.box);
-            if (lane == 0) mbar_expect_tx(bar, (uint32_t)used * p.box * D * 2);
+            const int used = min(PF_UNIT, (left + p.box - 1) / p.box * p.box);  // rows
+            if (lane == 0) mbar_expect_tx(bar, (uint32_t)used * D * 2);
             __syncwarp();
-            if (lane < used) {
-              const int r = row + lane * p.box;
-              long long y = kv_row_of(a.kv, b, h, r);
-              if (y < 0) y = (long long)a.kv.n_blocks * a.kv.Hkv * a.kv.block;  // outside: zeros
+            if ((int)my_box < used) {
+              const int r = (row + (int)my_box) & in_block;
+              long long y = ((long long)blk * a.kv.Hkv + w.h) * a.kv.block + r;
+              if ((unsigned)blk >= (unsigned)a.kv.n_blocks) {
+                kv_fail(MK_ERR_INVALID_ARG);
+                y = (long long)a.kv.n_blocks * a.kv.Hkv * a.kv.block;  // outside: zeros
+              }
 #pragma unroll
               for (int c = 0; c < C; c++)
-                tma_load_2d(dst + c * 16384 + lane * p.box * 128, is_v ? &vmap : &kmap, 64 * c, (int)y,
-                            bar, policy_evict_normal());
+                tma_load_2d(dst + c * 16384 + my_box * 128, map, 64 * c, (int)y, bar, policy);
             }
+            __syncwarp();
           }
-          n++;
         }
       }
-      if (!ok) {  // given up: wait for the copies in flight, again with a limit
+      if (sh.abort) {  // given up: wait for the copies in flight, again with a limit
         const unsigned long long t0 = gtimer();
-        for (uint32_t i = n > Sh::STAGES ? n - Sh::STAGES : 0; i < n; i++)
-          while (!mbar_try(smem_u32(&sh.kv_full[i % Sh::STAGES]), (i / Sh::STAGES) & 1) &&
-                 gtimer() - t0 < PF_TIMEOUT_NS) {
+        for (uint32_t i = n > NS ? n - NS : 0; i < n; i++)
+          while (!mbar_try(smem_u32(&full[i % NS]), (i / NS) & 1) && gtimer() - t0 < PF_TIMEOUT_NS) {
           }
       }
     } else if (warp == 1) {
-      if (lane == 0) {
       // --------------------------------------------------------- products ----
-      uint32_t n = 0;              // stages taken
-      uint32_t ns[2] = {0, 0};     // S tiles made
-      uint32_t np[2] = {0, 0};     // P tiles taken
-      uint32_t jobs[2] = {0, 0};
+      // (the whole warp takes every step, so that addresses stay in uniform
+      // registers; one elected lane issues)
+      const bool lead = elect_one();
       const uint32_t id_qk = idesc_bf16(128, 128) | (p.negate ? 1u << 13 : 0u);
       const uint32_t id_pv = idesc_bf16(128, D) | (1u << 16);
+      const uint32_t q_desc = desc_lo(q_smem), k_desc = desc_lo(k_ring), v_desc = desc_lo_mn(v_ring);
+      uint32_t ks = 0, kp = 0, vs = 0, vp = 0;  // stages and their phases
+      uint32_t ph = 0;       // phase bits: 1 << t s_free, 4 << t p_full, 16 << t q_full, 64 << t o_empty
+      uint32_t used = 0;     // 1 << t: an S_t has been made, 4 << t: an O_t
       bool ok = true;
-      auto stage_wait = [&](uint32_t i) {
-        ok = ok && pf_wait(sh, &sh.kv_full[i % Sh::STAGES], i / Sh::STAGES);
+      PfRec w;
+      uint32_t taken = 0;
+      auto wait = [&](const unsigned long long* bar, uint32_t bit) {
+        ok = ok && __all_sync(0xFFFFFFFFu, pf_wait(sh, bar, (ph & bit) ? 1 : 0));
+        ph ^= bit;
       };
-      auto qk = [&](int t, uint32_t stage) {
-        if (SEP && ns[t] > 0) ok = ok && pf_wait(sh, &sh.s_free[t], ns[t] - 1);
+      auto qk = [&](int t) {
+        if (SEP) {
+          if (used & (1u << t)) wait(&sh.s_free[t], 1u << t);
+          used |= 1u << t;
+        }
         if (!ok) return;
         tc_fence_after();
-        {
-          const uint32_t kt = ring + (stage % Sh::STAGES) * Sh::TILE, qt = q_smem + t * Sh::TILE;
+        const uint32_t ad = q_desc + t * (Sh::TILE >> 4), bd = k_desc + ks * (Sh::TILE >> 4);
+        if (lead) {
 #pragma unroll
           for (int s = 0; s < D / 16; s++)
-            tc_mma_bf16(tmem + Sh::S_COL + 128 * t, sw128_desc(qt + (s >> 2) * 16384 + (s & 3) * 32),
-                        sw128_desc(kt + (s >> 2) * 16384 + (s & 3) * 32), id_qk, s > 0);
+            mma_ss(tmem + Sh::S_COL + 128 * t, ad + (s >> 2) * 1024 + (s & 3) * 2,
+                   bd + (s >> 2) * 1024 + (s & 3) * 2, id_qk, s > 0);
           tc_commit(smem_u32(&sh.s_full[t]));
         }
-        ns[t]++;
+        __syncwarp();
       };
-      auto pv = [&](int t, uint32_t stage, bool first) {
-        ok = ok && pf_wait(sh, &sh.p_full[t], np[t]);
-        if (first && jobs[t] > 0) ok = ok && pf_wait(sh, &sh.o_empty[t], jobs[t] - 1);
+      auto pv = [&](int t, bool first, bool last) {
+        wait(&sh.p_full[t], 4u << t);
+        if (first) {
+          if (used & (4u << t)) wait(&sh.o_empty[t], 64u << t);
+          used |= 4u << t;
+        }
         if (!ok) return;
         tc_fence_after();
-        {
-          const uint32_t vt = ring + (stage % Sh::STAGES) * Sh::TILE;
+        const uint32_t bd = v_desc + vs * (Sh::TILE >> 4);
+        if (lead) {
 #pragma unroll
           for (int s = 0; s < 8; s++)
-            tc_mma_ts(tmem + Sh::O_COL + D * t,
-                      tmem + (SEP ? Sh::P_COL + 64 * t : Sh::S_COL + 128 * t) + 8 * s,
-                      sw128_desc_mn(vt + s * 2048), id_pv, !first || s > 0);
-          tc_commit(smem_u32(&sh.pv_done[t]));
+            mma_ts(tmem + Sh::O_COL + D * t, tmem + (SEP ? Sh::P_COL + 64 * t : Sh::S_COL + 128 * t) + 8 * s,
+                   bd + s * 128, id_pv, !first || s > 0);
+          if (SEP || last) tc_commit(smem_u32(&sh.pv_done[t]));
         }
-        np[t]++;
+        __syncwarp();
       };
-      auto release = [&](uint32_t stage) {
-        if (ok) tc_commit(smem_u32(&sh.kv_empty[stage % Sh::STAGES]));
+      auto k_wait = [&]() { ok = ok && __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.k_full[ks], kp)); };
+      auto k_next = [&]() {
+        if (ok && lead) tc_commit(smem_u32(&sh.k_empty[ks]));
+        if (++ks == NS) { ks = 0; kp ^= 1; }
       };
-      for (; w.more && ok; sh.walk[1].next(p)) {
-        const int ka = w.ka, e0 = w.end_of(p, 0), e1 = w.end_of(p, 1), kb = max(e0, e1);
+      while (ok && pf_take(sh, taken, w, lane == 0)) {
+        const int ka = w.ka, e0 = w.e[0], e1 = w.e[1], kb = max(e0, e1);
         if (ka == kb) continue;
-        const int e[2] = {e0, e1};
-        stage_wait(n);
-#pragma unroll
-        for (int t = 0; t < 2; t++)
-          if (ka < e[t]) {
-            ok = ok && pf_wait(sh, &sh.q_full[t], jobs[t]);
-            qk(t, n);
-            if (ok && ka + 1 == e[t]) tc_commit(smem_u32(&sh.q_empty[t]));
-          }
-        release(n);
-        n++;
+        k_wait();
+        if (ka < e0) {
+          wait(&sh.q_full[0], 16u);
+          qk(0);
+        }
+        if (ka < e1) {
+          wait(&sh.q_full[1], 32u);
+          qk(1);
+        }
+        k_next();
         for (int j = ka; j < kb && ok; j++) {
           const bool next = j + 1 < kb;
-          // stages of V(j) and K(j + 1) in the order of their loading
-          const uint32_t sv = n + (SEP && next ? 1 : 0), sk = n + (SEP ? 0 : 1);
           if (SEP && next) {
-            stage_wait(sk);
-#pragma unroll
-            for (int t = 0; t < 2; t++)
-              if (j + 1 < e[t]) {
-                qk(t, sk);
-                if (ok && j + 2 == e[t]) tc_commit(smem_u32(&sh.q_empty[t]));
-              }
-            release(sk);
+            k_wait();
+            if (j + 1 < e0) qk(0);
+            if (j + 1 < e1) qk(1);
+            k_next();
           }
-          stage_wait(sv);
-#pragma unroll
-          for (int t = 0; t < 2; t++) {
-            if (j < e[t]) pv(t, sv, j == ka);
-            if (!SEP && j + 1 < e[t]) {
-              stage_wait(sk);
-              qk(t, sk);
-              if (ok && j + 2 == e[t]) tc_commit(smem_u32(&sh.q_empty[t]));
-            }
-          }
-          release(sv);
-          if (!SEP && next) release(sk);
-          n += next ? 2 : 1;
+          ok = ok && __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.v_full[vs], vp));
+          if (j < e0) pv(0, j == ka, j + 1 == e0);
+          if (!SEP && next) k_wait();
+          if (!SEP && j + 1 < e0) qk(0);
+          if (j < e1) pv(1, j == ka, j + 1 == e1);
+          if (ok && lead) tc_commit(smem_u32(&sh.v_empty[vs]));
+          if (++vs == NS) { vs = 0; vp ^= 1; }
+          if (!SEP && j + 1 < e1) qk(1);
+          if (!SEP && next) k_next();
         }
-#pragma unroll
-        for (int t = 0; t < 2; t++)
-          if (ka < e[t]) jobs[t]++;
       }
       // the products in flight still read shared and write tensor memory
-      tc_commit(smem_u32(&sh.drain));
+      if (lead) tc_commit(smem_u32(&sh.drain));
       const unsigned long long t0 = gtimer();
       while (!mbar_try(smem_u32(&sh.drain), 0) && gtimer() - t0 < PF_TIMEOUT_NS) {
       }
-      }
     } else {
-      // ------------------------------------------------------------- queries ----
-      uint32_t jobs[2] = {0, 0};
-      bool ok = true;
-      const int i0 = threadIdx.x - 64;
-      for (; w.more && ok; next_job()) {
-        for (int t = 0; t < 2 && ok; t++) {
-          if (w.end_of(p, t) == w.ka) continue;
-          if (jobs[t] > 0) ok = __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.q_empty[t], jobs[t] - 1));
-          if (!ok) break;
-          jobs[t]++;
-          const int rows = w.rows(p, t), token0 = w.job.s.first + w.job.j * p.tokens;
-          const uint32_t dst = q_smem + t * Sh::TILE;
-          const uint16_t* src = (const uint16_t*)a.q.p + (long long)w.job.h * a.G * a.q.hs;
-          for (int c = i0; c < 128 * (D / 8); c += 64) {
-            const int r = c / (D / 8), k = c % (D / 8), row = 128 * t + r;
-            const int token = token0 + row / a.G, g = row % a.G;
-            const bool in = r < rows;
-            cp_async16_zfill(dst + (k >> 3) * 16384 + r * 128 + (((k ^ r) & 7) << 4),
-                             in ? src + token * a.q.ts + g * a.q.hs + k * 8 : src, in);
+      // -------------------------------------------------------------- jobs ----
+      PfWalk walk;
+      walk.begin(p, blockIdx.x, lane);
+      for (uint32_t n = 0;; n++) {
+        const int i = n % PF_RECS;
+        bool ok = true;
+        if (n >= PF_RECS) ok = pf_wait(sh, &sh.rec_empty[i], n / PF_RECS - 1);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        if (lane == 0) {
+          PfRec r{};
+          r.b = -1;
+          if (walk.more) {
+            r.b = walk.job.s.b;
+            r.h = walk.job.h;
+            r.len = walk.job.s.len;
+            const int token = walk.job.j * p.tokens;
+            r.row = walk.job.s.first + token;
+            r.pos = walk.job.s.len - walk.job.s.n + token;
+            r.ka = walk.ka;
+            for (int t = 0; t < 2; t++) {
+              r.rows[t] = walk.rows(p, t);
+              r.e[t] = walk.end_of(p, t);
+            }
+            r.whole = walk.whole;
+            r.slot = walk.first ? 0 : 1;
           }
-          cp_async_wait_all();
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[t]));
+          sh.rec[i] = r;
+          mbar_arrive(smem_u32(&sh.rec_full[i]));
         }
+        __syncwarp();
+        if (!walk.more) break;
+        walk.next(p);
       }
     }
   } else {
@@ -617,19 +714,41 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
     const uint32_t s_addr = tmem + lane_base + Sh::S_COL + 128 * t;
     const uint32_t o_addr = tmem + lane_base + Sh::O_COL + D * t;
     const uint32_t p_addr = SEP ? tmem + lane_base + Sh::P_COL + 64 * t : s_addr;
-    uint32_t n = 0;  // S tiles taken
+    const int row = 128 * t + r, row_token = row / a.G, row_head = row % a.G;
+    uint32_t taken = 0, sp = 0, vp = 0;  // records taken; phases of s_full and pv_done
     bool ok = true;
-    for (; w.more && ok; next_job()) {
-      const int rows = w.rows(p, t);
-      if (rows <= 0) continue;
-      const int ka = w.ka, kb = w.end_of(p, t);
-      const int row = 128 * t + r, token = w.job.j * p.tokens + row / a.G;
+    PfRec w, nx;
+    // A job's row of queries, one per thread, into the swizzled tile.  The tile is
+    // free as soon as the last S of the job before is there.
+    auto load_q = [&](const PfRec& x) {
+      const bool in = r < (t == 0 ? x.rows[0] : x.rows[1]);
+      const uint16_t* src = (const uint16_t*)a.q.p;
+      if (in) src += (x.row + row_token) * a.q.ts + ((long long)x.h * a.G + row_head) * a.q.hs;
+      const uint32_t dst = q_smem + t * Sh::TILE + r * 128;
+#pragma unroll
+      for (int k = 0; k < D / 8; k++)
+        cp_async16_zfill(dst + (k >> 3) * 16384 + (((k ^ r) & 7) << 4), src + (in ? 8 * k : 0), in);
+    };
+    auto units = [&](const PfRec& x) { return (t == 0 ? x.e[0] : x.e[1]) - x.ka; };
+    bool more = pf_take(sh, taken, w, lane == 0);
+    if (more && units(w) > 0) load_q(w);
+    while (more) {
+      const int rows = t == 0 ? w.rows[0] : w.rows[1];
+      const int ka = w.ka, kb = ka + units(w);
+      nx.b = -1;
       // the last cache row this row sees (rows that do not exist: every one)
-      const int last = r < rows ? w.job.s.len - w.job.s.n + token : 0x3FFFFFFF;
+      const int last = r < rows ? w.pos + row_token : 0x3FFFFFFF;
       float m = -INFINITY, l = 0.f;
+      if (kb > ka) {
+        cp_async_wait_all();
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[t]));
+      }
       for (int j = ka; j < kb; j++) {
-        ok = __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.s_full[t], n));
+        ok = __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.s_full[t], sp));
         if (!ok) break;
+        sp ^= 1;
         tc_fence_after();
         uint32_t x[128];
         tmem_ld64(s_addr, x);
@@ -652,11 +771,13 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
           mx1 = max3(mx1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
         }
         const float mx = max3(fmaxf(mx0, mx1), __uint_as_float(x[126]), __uint_as_float(x[127])) * p.scale2;
-        // O and P are this thread's to write once the product before is done
+        // O and P are this thread's to write once the product before is done (where
+        // P takes S's place, this S is the sign of it)
         const bool higher = mx > m + 8.f, raise = __any_sync(0xFFFFFFFFu, higher);
-        if (j > ka && (SEP || raise)) {
-          ok = __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.pv_done[t], n - 1));
+        if (SEP && j > ka) {
+          ok = __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.pv_done[t], vp));
           if (!ok) break;
+          vp ^= 1;
           tc_fence_after();
         }
         if (raise) {
@@ -697,19 +818,26 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[t]));
-        n++;
+        if (j == kb - 1) {  // while the last product runs: the next job's queries
+          if (pf_take(sh, taken, nx, lane == 0)) {
+            if (units(nx) > 0) load_q(nx);
+          } else {
+            nx.b = -2;
+          }
+        }
       }
       if (!ok) break;
       // -- the job's end: out = o / l, or a partial state
       if (kb > ka) {
-        ok = __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.pv_done[t], n - 1));
+        ok = __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.pv_done[t], vp));
         if (!ok) break;
+        vp ^= 1;
         tc_fence_after();
       }
       const bool mine = r < rows;
-      const int hq = w.job.h * a.G + row % a.G;
-      const long long tok = w.job.s.first + token;
-      float* st = a.ws + ((size_t)blockIdx.x * 2 + (w.first ? 0 : 1)) * Sh::STATE;
+      const int hq = w.h * a.G + row_head;
+      const long long tok = w.row + row_token;
+      float* st = a.ws + ((size_t)blockIdx.x * 2 + w.slot) * Sh::STATE;
       uint16_t* out = (uint16_t*)a.o.p + tok * a.o.ts + hq * a.o.hs;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float bad = 0.f;
@@ -759,11 +887,10 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
         redo &= redo - 1;
         const int rr = __shfl_sync(0xFFFFFFFFu, row, src);
         const int end = __shfl_sync(0xFFFFFFFFu, last, src) + 1;
-        const int tk = w.job.j * p.tokens + rr / a.G;
-        const int hh = w.job.h * a.G + rr % a.G;
-        const long long row_tok = w.job.s.first + tk;
+        const int hh = w.h * a.G + rr % a.G;
+        const long long row_tok = w.row + rr / a.G;
         float m1, l1, o1[D / 32];
-        attn_row<D>(a.kv, w.job.s.b, w.job.h, (const uint16_t*)a.q.p + row_tok * a.q.ts + hh * a.q.hs,
+        attn_row<D>(a.kv, w.b, w.h, (const uint16_t*)a.q.p + row_tok * a.q.ts + hh * a.q.hs,
                     a.scale, ka * PF_UNIT, min(end, kb * PF_UNIT), m1, l1, o1);
         // a partial state keeps the row's m and l, which are sound
         const float f1 = w.whole ? (l1 == 0.f ? 0.f : 1.f / l1)
@@ -777,7 +904,14 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
             st[((size_t)(dim / 4) * PF_ROWS + rr) * 4 + dim % 4] = o1[e] * f1;
         }
       }
+      if (kb == ka) {
+        if (!pf_take(sh, taken, nx, lane == 0)) nx.b = -2;
+        else if (units(nx) > 0) load_q(nx);
+      }
+      more = nx.b >= 0;
+      w = nx;
     }
+    cp_async_wait_all();
   }
   __syncwarp();
   tc_fence_before();
@@ -796,15 +930,15 @@ __global__ void __launch_bounds__(256) kv_prefill_join_kernel(const __grid_const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = blockIdx.x + 1;
   const AttnArgs& a = p.a;
-  int parts;
-  const long long total = pf_total(p, blocks, lane, parts);
-  bool mine = i < parts;
+  const PfSeq s0 = pf_seq(p, lane);
+  const PfLine line = pf_line(p, blocks, lane, s0);
+  bool mine = i < line.parts;
   PfCut cut{};
   int slot = 0;
-  const long long share = total / max(parts, 1);
   if (mine) {
-    cut = pf_find(p, part_begin(total, parts, i), share, lane);
-    const PfCut prev = pf_find(p, part_begin(total, parts, i - 1), share, lane);
+    const PfCut both = pf_find(p, line.begin(i - 1), line.begin(i), line.snap, lane, s0);
+    const PfCut prev = pf_shfl(both, 0);
+    cut = pf_shfl(both, 1);
     const bool inside = cut.unit > 0 && cut.unit < PF_AFTER;
     const bool same = pf_same(prev.job, cut.job);
     mine = inside && !(same && prev.unit > 0 && prev.unit < PF_AFTER);
@@ -820,19 +954,17 @@ __global__ void __launch_bounds__(256) kv_prefill_join_kernel(const __grid_const
   const int row = 32 * blockIdx.y + lane;
   const int n_rows = min(p.tokens, cut.job.s.n - cut.job.j * p.tokens) * a.G;
   const bool live = row < n_rows;
-  const long long start = part_begin(total, parts, i) - cut.off;  // of the job on the line
+  const long long start = line.begin(i) - cut.off;  // of the job on the line
   float m = -INFINITY, l = 0.f;
   float4 o[N];
 #pragma unroll
   for (int c = 0; c < N; c++) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const long long size = pf_before(p, cut.job.s, cut.job.j + 1) - pf_before(p, cut.job.s, cut.job.j);
   int unit = 0;  // where the part begins
   for (int k = i - 1;; k++) {
     // part k ends at cut k + 1
-    const int next = k + 1 >= parts ? PF_AFTER
-                                    : pf_unit_at(p, cut.job, part_begin(total, parts, k + 1) - start, share);
-    const bool beyond = k + 1 >= parts ||
-        part_begin(total, parts, k + 1) - start >= pf_before(p, cut.job.s, cut.job.j + 1) - pf_before(p, cut.job.s, cut.job.j);
-    const int until = beyond ? PF_AFTER : next;
+    const long long off = line.begin(k + 1) - start;
+    const int until = k + 1 >= line.parts || off >= size ? PF_AFTER : pf_unit_at(p, cut.job, off, line.snap);
     if (until > unit && live) {
       const float* st = a.ws + ((size_t)k * 2 + (k == i - 1 ? slot : 0)) * Sh::STATE;
       const float mi = st[PF_ROWS * D + row], li = st[PF_ROWS * D + PF_ROWS + row];
