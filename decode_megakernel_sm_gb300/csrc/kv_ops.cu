@@ -1,5 +1,6 @@
 // kv_ops.cu -- the KV-cache operators' entry points: checks of the arguments,
 // choice of the kernel, launch.  No state, no allocation.
+#include <atomic>
 #include <cmath>
 
 #include <cuda_runtime.h>
@@ -76,12 +77,21 @@ static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 // Whether the kernel was compiled to the registers its warps deal out among
 // themselves (fewer would leave them waiting), and may use its shared memory.
+// Found once per device.
 template <int D>
 static bool prefill_ready() {
+  static std::atomic<uint64_t> known{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (known.load(std::memory_order_relaxed) & bit) return true;
   cudaFuncAttributes at{};
-  return cudaFuncGetAttributes(&at, kv_prefill_kernel<D>) == cudaSuccess && at.numRegs == PF_REGS &&
-         cudaFuncSetAttribute(kv_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              PfShape<D>::SMEM) == cudaSuccess;
+  if (cudaFuncGetAttributes(&at, kv_prefill_kernel<D>) != cudaSuccess || at.numRegs != PF_REGS ||
+      cudaFuncSetAttribute(kv_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           PfShape<D>::SMEM) != cudaSuccess)
+    return false;
+  if (dev < 64) known.fetch_or(bit, std::memory_order_relaxed);
+  return true;
 }
 
 template <int D>
@@ -92,12 +102,12 @@ static int prefill_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
   if (rows >= 0x7FFFFFFFll) return MK_ERR_UNSUPPORTED;
   PfArgs p{};
   p.a = a;
-  p.tokens = PF_ROWS / a.G;
+  p.tokens = PF_ROWS / 2 / a.G * 2;
   p.negate = a.scale < 0.f;
   // (a scale of zero: so small that every finite score rounds to the same weight)
   p.scale2 = std::fmax(std::fabs(a.scale) * LOG2E, 1e-30f);
   p.box = a.kv.table && a.kv.block < PF_UNIT ? a.kv.block : PF_UNIT;
-  CUtensorMap maps[2];
+  CUtensorMap maps[3];
   const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)D * 2};
   const cuuint32_t box[2] = {64, (cuuint32_t)p.box}, es[2] = {1, 1};
   for (int i = 0; i < 2; i++)
@@ -105,7 +115,15 @@ static int prefill_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return MK_ERR_CUDA;
-  kv_prefill_kernel<D><<<n_sm, PF_THREADS, PfShape<D>::SMEM, s>>>(p, maps[0], maps[1]);
+  // queries: [token][head][D], boxes of a tile's tokens and one kv head's heads
+  const cuuint64_t qdims[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)a.bt.n_tokens};
+  const cuuint64_t qstrides[2] = {(cuuint64_t)(a.q.hs * 2), (cuuint64_t)(a.q.ts * 2)};
+  const cuuint32_t qbox[3] = {64, (cuuint32_t)a.G, (cuuint32_t)p.tokens / 2}, qes[3] = {1, 1, 1};
+  if (enc(&maps[2], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q.p, qdims, qstrides, qbox, qes,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return MK_ERR_CUDA;
+  kv_prefill_kernel<D><<<n_sm, PF_THREADS, PfShape<D>::SMEM, s>>>(p, maps[0], maps[1], maps[2]);
   if (n_sm > 1 && launch_dependent(kv_prefill_join_kernel<D>, dim3(n_sm - 1, PF_ROWS / 32), 256, s,
                                    p, n_sm) != cudaSuccess)
     return MK_ERR_CUDA;
@@ -212,7 +230,8 @@ extern "C" int mk_attn_workspace_bytes(int decode, int n_tokens, int batch, int 
   const int n = sm_count(), nt = decode_tiles(n_q_heads / n_kv_heads);
   if (n == 0) return MK_ERR_CUDA;
   if (!decode) {
-    *bytes = (head_dim == 64 ? PfShape<64>::STATE : PfShape<128>::STATE) * sizeof(float) * 2 * n;
+    *bytes = ((head_dim == 64 ? PfShape<64>::STATE : PfShape<128>::STATE) * sizeof(float) * 2 +
+              sizeof(PfPart)) * n;
   } else {
     *bytes = head_dim == 64 ? (nt == 1 ? decode_ws<64, 1>(n) : decode_ws<64, 2>(n))
                             : (nt == 1 ? decode_ws<128, 1>(n) : decode_ws<128, 2>(n));

@@ -2,24 +2,24 @@
 // its cache rows, on the fifth-generation tensor cores.
 //
 // Rows and jobs.  The G query heads of a kv head read the same keys, so a row
-// of the matrix product is a (token, head) pair, row = token * G + head, and a
-// job is up to 256 rows (floor(256 / G) whole tokens) of one sequence and kv
-// head: two tiles of 128 rows, the tensor core's M, which share every key and
+// of the matrix product is a (token, head) pair: a tile is floor(128 / G) whole
+// tokens, row = token * G + head, in the 128 rows of a tensor-core product, and a
+// job is two such tiles of one sequence and kv head, which share every key and
 // value tile.  A key tile is 128 cache rows (a unit of a job's work).
 //
 // One block per SM runs a piece of the line of all jobs:
-//   warps 0, 2  load key tiles (0) and value tiles (2) into rings of stages
-//               (tiled TMA, one box per page piece, 128-byte swizzle)
-//   warp 1      issues the products: S_t = Q_t K^T and O_t += P_t V, both with
-//               the accumulator in tensor memory; P is the A operand straight
-//               from tensor memory, V the transposed (MN-major) B operand
-//   warp 3      walks the block's piece of the line and posts one record per job
+//   warps 0, 2  load key tiles (0), query and value tiles (2) (tiled TMA, keys and
+//               values one box per page piece, 128-byte swizzle); warp 0 also
+//               walks the block's piece of the line and posts one record per job
 //               in a ring, so that the others do no arithmetic on jobs
-//   warps 4-7   softmax of tile 0, one row per thread: the row's queries into
-//               shared memory, S from tensor memory to registers, running maximum
-//               and sum in fp32, P (bf16) back to tensor memory; O's rescale,
-//               where a maximum rises by more than 2^8 (rare after the first
-//               tiles), and the results
+//   warps 1, 3  issue the products of tile 0 and of tile 1: S_t = Q_t K^T and
+//               O_t += P_t V, both with the accumulator in tensor memory; P is the
+//               A operand straight from tensor memory, V the transposed (MN-major)
+//               B operand.  A warp each, so that neither tile waits for the other
+//   warps 4-7   softmax of tile 0, one row per thread: S from tensor memory to
+//               registers, running maximum and sum in fp32, P (bf16) back to
+//               tensor memory; O's rescale, where a maximum rises by more than
+//               2^8 (rare after the first tiles), and the results
 //   warps 8-11  the same for tile 1
 // The two tiles take turns: the tensor cores work on one while the other's
 // softmax runs.  64-dim heads leave tensor memory for P beside S, so that the
@@ -61,6 +61,7 @@ constexpr int PF_UNIT = 128;      // cache rows of a unit
 constexpr int PF_JOB_COST = 256;  // a job's start and end, in keys
 constexpr int PF_MIN_SHARE = 4 * PF_UNIT;  // a part of a job is not worth less
 constexpr int PF_SNAP = 16;       // a cut this part of a share from a job's border moves there
+constexpr int PF_STAGGER = 2000;  // cycles
 constexpr int PF_AFTER = 1 << 30;
 constexpr unsigned long long PF_TIMEOUT_NS = 2000000000ull;
 
@@ -74,9 +75,16 @@ struct PfShape {
   static constexpr size_t STATE = (size_t)PF_ROWS * (D + 2);  // floats: o [D/4][256][4], m, l [256]
 };
 
+// Scratch: two partial states per block, then what each block's piece begins with.
+struct PfPart {
+  int b, h, j;       // its first job
+  int inside, more;  // it begins inside that job; it holds anything
+  int row, rows[2];  // of the job: first token's row of q, rows of its tiles
+};
+
 struct PfArgs {
   AttnArgs a;
-  int tokens;    // per job
+  int tokens;    // per job (two tiles)
   int negate;    // the scale is negative: scale2 is its magnitude, Q K^T is negated
   float scale2;  // |scale| log2 e
   int box;       // rows of a TMA box
@@ -252,6 +260,15 @@ MK_DEV bool pf_same(const PfJob& x, const PfJob& y) {
   return x.s.b == y.s.b && x.h == y.h && x.j == y.j;
 }
 
+// What the roles need to know about a job, and how they pass it on.
+struct PfRec {
+  int b, h, len;        // sequence, kv head, cache rows (b < 0: no more jobs)
+  int row, pos;         // first token of the job: its row of q, its position
+  int ka, e[2];         // units [ka, e[t]) for tile t
+  int rows[2];          // rows of tile t (none: <= 0)
+  int whole, slot;      // all units of the job; slot of its partial state
+};
+
 // A block's way along its piece of the line.
 struct PfWalk {
   PfJob job;
@@ -259,19 +276,22 @@ struct PfWalk {
   int ka, kb;       // units of the present job
   bool whole;       // all of them
   bool first;       // the piece's first job
+  bool inside;      // the piece begins inside a job
   bool more;
 
   MK_DEV void begin(const PfArgs& p, int part, int lane) {
     const PfSeq s0 = pf_seq(p, lane);
     const PfLine line = pf_line(p, gridDim.x, lane, s0);
-    more = false;
+    more = inside = false;
+    job.s.b = -1;
     if (part >= line.parts) return;
     const PfCut both = pf_find(p, line.begin(part), line.begin(part + 1), line.snap, lane, s0);
     const PfCut c = pf_shfl(both, 0);
     end = pf_shfl(both, 1);
-    if (pf_same(c.job, end.job) && c.unit == end.unit) return;
     job = c.job;
     ka = c.unit;
+    inside = ka > 0 && ka < PF_AFTER;
+    if (pf_same(c.job, end.job) && c.unit == end.unit) return;
     if (ka == PF_AFTER) {
       pf_next(p, job);
       ka = 0;
@@ -299,40 +319,61 @@ struct PfWalk {
     ka = 0;
     settle(p);
   }
-  // Rows of tile t, and the end of the units that it takes part in.
-  MK_DEV int rows(const PfArgs& p, int t) const {
-    const int n = min(p.tokens, job.s.n - job.j * p.tokens) * p.a.G;
-    return min(128, n - 128 * t);
+  // The present job, or the end.
+  MK_DEV void record(const PfArgs& p, PfRec& r) const {
+    r.b = -1;
+    if (!more) return;
+    r.b = job.s.b;
+    r.h = job.h;
+    r.len = job.s.len;
+    const int token = job.j * p.tokens;
+    r.row = job.s.first + token;
+    r.pos = job.s.len - job.s.n + token;
+    r.ka = ka;
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+      r.rows[t] = tokens_of(p, t) * p.a.G;
+      r.e[t] = end_of(p, t);
+    }
+    r.whole = whole;
+    r.slot = first ? 0 : 1;
+  }
+  // What the join needs to know of the piece (at its beginning).
+  MK_DEV void part(const PfArgs& p, PfPart& r) const {
+    r.b = job.s.b;
+    r.h = job.h;
+    r.j = job.j;
+    r.inside = inside;
+    r.more = more;
+    r.row = job.s.first + job.j * p.tokens;
+    r.rows[0] = tokens_of(p, 0) * p.a.G;
+    r.rows[1] = tokens_of(p, 1) * p.a.G;
+  }
+  // Tokens of tile t, and the end of the units that it takes part in.
+  MK_DEV int tokens_of(const PfArgs& p, int t) const {
+    const int per = p.tokens / 2;
+    return min(per, job.s.n - job.j * p.tokens - t * per);
   }
   MK_DEV int end_of(const PfArgs& p, int t) const {
-    const int n = rows(p, t);
+    const int n = tokens_of(p, t);
     if (n <= 0) return ka;
-    const int token = job.j * p.tokens + (128 * t + n - 1) / p.a.G;
-    return max(ka, min(kb, (pf_seen(job.s, token) + PF_UNIT - 1) / PF_UNIT));
+    const int last = job.j * p.tokens + t * (p.tokens / 2) + n - 1;
+    return max(ka, min(kb, (pf_seen(job.s, last) + PF_UNIT - 1) / PF_UNIT));
   }
 };
 
 // ---- small pieces ----------------------------------------------------------
-// What the roles need to know about a job, and how they pass it on.
-struct PfRec {
-  int b, h, len;        // sequence, kv head, cache rows (b < 0: no more jobs)
-  int row, pos;         // first token of the job: its row of q, its position
-  int ka, e[2];         // units [ka, e[t]) for tile t
-  int rows[2];          // rows of tile t (none: <= 0)
-  int whole, slot;      // all units of the job; slot of its partial state
-};
-
 constexpr int PF_RECS = 4;
-constexpr int PF_READERS = 11;  // warps that read the records (all but warp 3)
 
 struct PfShared {
   alignas(8) unsigned long long k_full[4], k_empty[4], v_full[4], v_empty[4];
   unsigned long long rec_full[PF_RECS], rec_empty[PF_RECS];
-  unsigned long long q_full[2], s_full[2], s_free[2], p_full[2], pv_done[2], o_empty[2];
+  unsigned long long q_full[2], q_empty[2], s_full[2], s_free[2], p_half[2], p_full[2], pv_done[2], o_empty[2];
   unsigned long long drain;
   PfRec rec[PF_RECS];
   uint32_t tmem;
   volatile int abort;
+  volatile uint32_t progress;  // S tiles that tile 0's softmax has half done
 };
 
 // Wait for phase `n` (counted from 0) of a barrier; false if the block gave up.
@@ -364,6 +405,15 @@ MK_DEV bool pf_take(PfShared& sh, uint32_t& n, PfRec& r, bool lead) {
   if (lead) mbar_arrive(smem_u32(&sh.rec_empty[i]));
   n++;
   return r.b >= 0;
+}
+
+// Tiled 3-D TMA load of one box, as tma_load_2d.
+MK_DEV void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+      : "memory");
 }
 
 // Low and high words of shared-memory matrix descriptors in the 128-byte
@@ -401,22 +451,29 @@ MK_DEV bool elect_one() {
 
 #define PF_R4(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3])
 #define PF_R16(x, i) PF_R4(x, i), PF_R4(x, i + 4), PF_R4(x, i + 8), PF_R4(x, i + 12)
+#define PF_U4(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3])
+#define PF_U16(x, i) PF_U4(x, i), PF_U4(x, i + 4), PF_U4(x, i + 8), PF_U4(x, i + 12)
 #define PF_I4(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3])
 #define PF_I16(x, i) PF_I4(x, i), PF_I4(x, i + 4), PF_I4(x, i + 8), PF_I4(x, i + 12)
 
-// 64 consecutive columns of this thread's tensor-memory lane, and the wait for
-// them in the same statement.
+// 64 consecutive columns of this thread's tensor-memory lane; they are there
+// after tmem_ld64_wait, which all uses depend on.
 MK_DEV void tmem_ld64(uint32_t addr, uint32_t* x) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n"
-      "tcgen05.wait::ld.sync.aligned;"
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
+      "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, "
+      "%36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, "
+      "%53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
       : PF_R16(x, 0), PF_R16(x, 16), PF_R16(x, 32), PF_R16(x, 48)
       : "r"(addr)
       : "memory");
 }
+MK_DEV void tmem_ld64_wait(uint32_t* x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : PF_U16(x, 0), PF_U16(x, 16), PF_U16(x, 32), PF_U16(x, 48)::"memory");
+}
+
 MK_DEV void tmem_ld32(uint32_t addr, uint32_t* x) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
@@ -443,6 +500,28 @@ MK_DEV float max3(float a, float b, float c) {
   return d;
 }
 
+// The largest of 64 floats (NaN counts as none).
+MK_DEV float max64(const uint32_t* x) {
+  float m[4];
+#pragma unroll
+  for (int c = 0; c < 4; c++) {
+    m[c] = fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 4]));
+#pragma unroll
+    for (int i = 8; i < 64; i += 8)
+      m[c] = max3(m[c], __uint_as_float(x[i + c]), __uint_as_float(x[i + c + 4]));
+  }
+  return max3(fmaxf(m[0], m[1]), m[2], m[3]);
+}
+
+// -inf in the places behind `limit` (one warp: nothing to do where no lane's
+// limit is below the last).
+MK_DEV void mask32(uint32_t* x, int limit) {
+  if (!__any_sync(0xFFFFFFFFu, limit < 31)) return;
+#pragma unroll
+  for (int i = 0; i < 32; i++)
+    if (i > limit) x[i] = 0xFF800000u;
+}
+
 // 2^x to about 2 units in the last place; results below 2^-126 are zero.
 MK_DEV float ex2(float x) {
   float y;
@@ -458,7 +537,7 @@ MK_DEV void cp_async16_zfill(uint32_t dst, const void* src, bool in) {
 template <int D>
 __global__ void __launch_bounds__(PF_THREADS, 1)
 kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUtensorMap kmap,
-                  const __grid_constant__ CUtensorMap vmap) {
+                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap) {
   using Sh = PfShape<D>;
   constexpr int C = D / 64;  // 64-column halves of a tile
   constexpr bool SEP = Sh::SEP;
@@ -473,24 +552,27 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; i++) {
       mbar_init(smem_u32(&sh.k_full[i]), 1);
-      mbar_init(smem_u32(&sh.k_empty[i]), 1);
+      mbar_init(smem_u32(&sh.k_empty[i]), SEP ? 2 : 1);
       mbar_init(smem_u32(&sh.v_full[i]), 1);
-      mbar_init(smem_u32(&sh.v_empty[i]), 1);
+      mbar_init(smem_u32(&sh.v_empty[i]), SEP ? 2 : 1);
     }
     for (int i = 0; i < PF_RECS; i++) {
       mbar_init(smem_u32(&sh.rec_full[i]), 1);
-      mbar_init(smem_u32(&sh.rec_empty[i]), PF_READERS);
+      mbar_init(smem_u32(&sh.rec_empty[i]), SEP ? 11 : 10);  // the warps that read it
     }
     for (int t = 0; t < 2; t++) {
-      mbar_init(smem_u32(&sh.q_full[t]), 4);
+      mbar_init(smem_u32(&sh.q_full[t]), 1);
+      mbar_init(smem_u32(&sh.q_empty[t]), 1);
       mbar_init(smem_u32(&sh.s_full[t]), 1);
       mbar_init(smem_u32(&sh.s_free[t]), 4);
+      mbar_init(smem_u32(&sh.p_half[t]), 4);
       mbar_init(smem_u32(&sh.p_full[t]), 4);
       mbar_init(smem_u32(&sh.pv_done[t]), 1);
       mbar_init(smem_u32(&sh.o_empty[t]), 4);
     }
-    mbar_init(smem_u32(&sh.drain), 1);
+    mbar_init(smem_u32(&sh.drain), 2);
     sh.abort = 0;
+    sh.progress = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), 512);
@@ -499,6 +581,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const AttnArgs& a = p.a;
+  PfPart* parts = (PfPart*)(a.ws + (size_t)gridDim.x * 2 * Sh::STATE);
 
   // The block's registers, PF_REGS x 384, are dealt out anew: 128 x 104 + 256 x 200.
   if (warp < 4) {
@@ -513,12 +596,58 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
       const uint64_t policy = policy_evict_normal();
       const int shift = a.kv.shift, in_block = a.kv.table ? a.kv.block - 1 : 0x7FFFFFFF;
       const uint32_t my_box = (uint32_t)lane * p.box;
-      uint32_t n = 0, taken = 0;  // stages filled, records taken
+      uint32_t n = 0, taken = 0;  // stages filled, records taken (or posted)
       bool ok = true;
       PfRec w;
-      while (ok && pf_take(sh, taken, w, lane == 0)) {
+      uint32_t q_used = 0, q_phase = 0;  // by tile: loaded before; phase of q_empty
+      PfWalk walk;
+      if (!is_v) {
+        walk.begin(p, blockIdx.x, lane);
+        if (lane == 0) walk.part(p, parts[blockIdx.x]);
+      }
+      // Warp 0: the present job's record, for itself and the other warps; the one
+      // after the last job says so.
+      auto post = [&]() {
+        const int i = taken % PF_RECS;
+        if (taken >= PF_RECS && !__all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.rec_empty[i], taken / PF_RECS - 1)))
+          return false;
+        walk.record(p, w);
+        if (lane == 0) {
+          sh.rec[i] = w;
+          mbar_arrive(smem_u32(&sh.rec_full[i]));
+        }
+        __syncwarp();
+        taken++;
+        return w.b >= 0;
+      };
+      while (ok && (is_v ? pf_take(sh, taken, w, lane == 0) : post())) {
         const int kb = max(w.e[0], w.e[1]);
-        if (kb == w.ka) continue;
+        if (kb == w.ka) {
+          if (!is_v) walk.next(p);
+          continue;
+        }
+        if (is_v) {  // the queries: one box of whole tokens and their heads per tile
+          const int tile_rows = p.tokens / 2 * a.G;
+#pragma unroll
+          for (int t = 0; t < 2; t++) {
+            if (w.e[t] == w.ka) continue;
+            if (q_used >> t & 1) {
+              ok = ok && __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.q_empty[t], q_phase >> t & 1));
+              q_phase ^= 1u << t;
+            }
+            q_used |= 1u << t;
+            if (ok && lane == 0) {
+              const uint32_t bar = smem_u32(&sh.q_full[t]), dst = q_smem + t * Sh::TILE;
+              mbar_expect_tx(bar, (uint32_t)tile_rows * D * 2);
+#pragma unroll
+              for (int c = 0; c < C; c++)
+                tma_load_3d(dst + c * 16384, &qmap, 64 * c, w.h * a.G, w.row + t * (p.tokens / 2), bar,
+                            policy);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+        }
         // Block of this lane's box of a unit, looked up one unit ahead; a lane
         // whose box begins behind the sequence's end has none to load.
         const int* table = a.kv.table + (size_t)w.b * a.kv.table_stride;
@@ -567,6 +696,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
             }
             __syncwarp();
           }
+          if (!is_v && j == w.ka) walk.next(p);  // while the copy runs
         }
       }
       if (sh.abort) {  // given up: wait for the copies in flight, again with a limit
@@ -574,8 +704,12 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
         for (uint32_t i = n > NS ? n - NS : 0; i < n; i++)
           while (!mbar_try(smem_u32(&full[i % NS]), (i / NS) & 1) && gtimer() - t0 < PF_TIMEOUT_NS) {
           }
+        for (int t = 0; t < 2; t++)  // (the queries' last load has q_empty's phase)
+          while ((q_used >> t & 1) && !mbar_try(smem_u32(&sh.q_full[t]), q_phase >> t & 1) &&
+                 gtimer() - t0 < PF_TIMEOUT_NS) {
+          }
       }
-    } else if (warp == 1) {
+    } else {
       // --------------------------------------------------------- products ----
       // (the whole warp takes every step, so that addresses stay in uniform
       // registers; one elected lane issues)
@@ -584,19 +718,24 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
       const uint32_t id_pv = idesc_bf16(128, D) | (1u << 16);
       const uint32_t q_desc = desc_lo(q_smem), k_desc = desc_lo(k_ring), v_desc = desc_lo_mn(v_ring);
       uint32_t ks = 0, kp = 0, vs = 0, vp = 0;  // stages and their phases
-      uint32_t ph = 0;       // phase bits: 1 << t s_free, 4 << t p_full, 16 << t q_full, 64 << t o_empty
-      uint32_t used = 0;     // 1 << t: an S_t has been made, 4 << t: an O_t
+      // by tile, bit t: phases of s_free, p_half / p_full, q_full, o_empty; whether
+      // an S, an O has been made
+      uint32_t ph_s = 0, ph_p = 0, ph_q = 0, ph_o = 0, any_s = 0, any_o = 0;
+      uint32_t taken = 0, tiles0 = 0;  // records taken, S tiles that tile 0 had before
       bool ok = true;
       PfRec w;
-      uint32_t taken = 0;
-      auto wait = [&](const unsigned long long* bar, uint32_t bit) {
-        ok = ok && __all_sync(0xFFFFFFFFu, pf_wait(sh, bar, (ph & bit) ? 1 : 0));
-        ph ^= bit;
+      auto wait = [&](const unsigned long long* bar, uint32_t phase) {
+        ok = ok && __all_sync(0xFFFFFFFFu, pf_wait(sh, bar, phase));
       };
-      auto qk = [&](int t) {
+      auto wait_tile = [&](const unsigned long long* bars, uint32_t& phases, int t) {
+        wait(&bars[t], (phases >> t) & 1);
+        phases ^= 1u << t;
+      };
+      // S_t = Q_t K^T of the present key stage
+      auto qk = [&](int t, bool last) {
         if (SEP) {
-          if (used & (1u << t)) wait(&sh.s_free[t], 1u << t);
-          used |= 1u << t;
+          if (any_s >> t & 1) wait_tile(sh.s_free, ph_s, t);
+          any_s |= 1u << t;
         }
         if (!ok) return;
         tc_fence_after();
@@ -607,102 +746,109 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
             mma_ss(tmem + Sh::S_COL + 128 * t, ad + (s >> 2) * 1024 + (s & 3) * 2,
                    bd + (s >> 2) * 1024 + (s & 3) * 2, id_qk, s > 0);
           tc_commit(smem_u32(&sh.s_full[t]));
+          if (last) tc_commit(smem_u32(&sh.q_empty[t]));
         }
         __syncwarp();
       };
+      // O_t += P_t V of the present value stage (in halves as P comes, where S waits
+      // for the place that P has)
       auto pv = [&](int t, bool first, bool last) {
-        wait(&sh.p_full[t], 4u << t);
         if (first) {
-          if (used & (4u << t)) wait(&sh.o_empty[t], 64u << t);
-          used |= 4u << t;
+          if (any_o >> t & 1) wait_tile(sh.o_empty, ph_o, t);
+          any_o |= 1u << t;
         }
-        if (!ok) return;
-        tc_fence_after();
         const uint32_t bd = v_desc + vs * (Sh::TILE >> 4);
-        if (lead) {
+        const uint32_t o_col = tmem + Sh::O_COL + D * t;
+        const uint32_t p_col = tmem + (SEP ? Sh::P_COL + 64 * t : Sh::S_COL + 128 * t);
 #pragma unroll
-          for (int s = 0; s < 8; s++)
-            mma_ts(tmem + Sh::O_COL + D * t, tmem + (SEP ? Sh::P_COL + 64 * t : Sh::S_COL + 128 * t) + 8 * s,
-                   bd + s * 128, id_pv, !first || s > 0);
-          if (SEP || last) tc_commit(smem_u32(&sh.pv_done[t]));
+        for (int half = SEP ? 1 : 0; half < 2; half++) {
+          wait(half == 0 ? &sh.p_half[t] : &sh.p_full[t], (ph_p >> t) & 1);
+          if (!ok) return;
+          tc_fence_after();
+          if (lead) {
+#pragma unroll
+            for (int s = SEP ? 0 : 4 * half; s < 4 * half + 4; s++)
+              mma_ts(o_col, p_col + 8 * s, bd + s * 128, id_pv, !first || s > 0);
+          }
+          __syncwarp();
         }
+        ph_p ^= 1u << t;
+        if (lead && (SEP || last)) tc_commit(smem_u32(&sh.pv_done[t]));
         __syncwarp();
       };
-      auto k_wait = [&]() { ok = ok && __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.k_full[ks], kp)); };
+      auto k_wait = [&]() { wait(&sh.k_full[ks], kp); };
       auto k_next = [&]() {
         if (ok && lead) tc_commit(smem_u32(&sh.k_empty[ks]));
         if (++ks == NS) { ks = 0; kp ^= 1; }
       };
-      while (ok && pf_take(sh, taken, w, lane == 0)) {
-        const int ka = w.ka, e0 = w.e[0], e1 = w.e[1], kb = max(e0, e1);
-        if (ka == kb) continue;
-        k_wait();
-        if (ka < e0) {
-          wait(&sh.q_full[0], 16u);
-          qk(0);
-        }
-        if (ka < e1) {
-          wait(&sh.q_full[1], 32u);
-          qk(1);
-        }
-        k_next();
-        for (int j = ka; j < kb && ok; j++) {
-          const bool next = j + 1 < kb;
-          if (SEP && next) {
-            k_wait();
-            if (j + 1 < e0) qk(0);
-            if (j + 1 < e1) qk(1);
-            k_next();
+      auto v_next = [&]() {
+        if (ok && lead) tc_commit(smem_u32(&sh.v_empty[vs]));
+        if (++vs == NS) { vs = 0; vp ^= 1; }
+      };
+      if (SEP) {
+        // 64-dim heads, a warp per tile: the exponentials bound them, and neither
+        // tile's softmax may wait for the other's
+        const int t = warp >> 1;
+        while (ok && pf_take(sh, taken, w, lane == 0)) {
+          const int ka = w.ka, e = t == 0 ? w.e[0] : w.e[1], kb = max(w.e[0], w.e[1]);
+          if (ka == kb) continue;
+          if (ka < e) {
+            wait_tile(sh.q_full, ph_q, t);
+            // Tile 1 starts half a step behind tile 0, so that one's exponentials run
+            // beside the other's maxima and products; side by side they would stay
+            // side by side.  (A hint: it waits a microsecond at most.)
+            if (t == 1 && ka < w.e[0]) {
+              const long long t0 = clock64();
+              while ((int)(sh.progress - (tiles0 + 1)) < 0 && clock64() - t0 < PF_STAGGER) {
+              }
+              __syncwarp();
+            }
           }
-          ok = ok && __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.v_full[vs], vp));
-          if (j < e0) pv(0, j == ka, j + 1 == e0);
-          if (!SEP && next) k_wait();
-          if (!SEP && j + 1 < e0) qk(0);
-          if (j < e1) pv(1, j == ka, j + 1 == e1);
-          if (ok && lead) tc_commit(smem_u32(&sh.v_empty[vs]));
-          if (++vs == NS) { vs = 0; vp ^= 1; }
-          if (!SEP && j + 1 < e1) qk(1);
-          if (!SEP && next) k_next();
+          tiles0 += w.e[0] - ka;
+          for (int j = ka - 1; j < kb && ok; j++) {
+            if (j + 1 < kb) {
+              k_wait();
+              if (j + 1 < e) qk(t, j + 2 == e);
+              k_next();
+            }
+            if (j >= ka) {
+              wait(&sh.v_full[vs], vp);
+              if (j < e) pv(t, j == ka, j + 1 == e);
+              v_next();
+            }
+          }
+        }
+      } else if (warp == 1) {
+        // 128-dim heads, one warp: the products bound them, and the tiles take turns
+        while (ok && pf_take(sh, taken, w, lane == 0)) {
+          const int ka = w.ka, e0 = w.e[0], e1 = w.e[1], kb = max(e0, e1);
+          if (ka == kb) continue;
+          k_wait();
+          if (ka < e0) {
+            wait_tile(sh.q_full, ph_q, 0);
+            qk(0, ka + 1 == e0);
+          }
+          if (ka < e1) {
+            wait_tile(sh.q_full, ph_q, 1);
+            qk(1, ka + 1 == e1);
+          }
+          k_next();
+          for (int j = ka; j < kb && ok; j++) {
+            wait(&sh.v_full[vs], vp);
+            if (j < e0) pv(0, j == ka, j + 1 == e0);
+            if (j + 1 < kb) k_wait();
+            if (j + 1 < e0) qk(0, j + 2 == e0);
+            if (j < e1) pv(1, j == ka, j + 1 == e1);
+            v_next();
+            if (j + 1 < e1) qk(1, j + 2 == e1);
+            if (j + 1 < kb) k_next();
+          }
         }
       }
       // the products in flight still read shared and write tensor memory
       if (lead) tc_commit(smem_u32(&sh.drain));
       const unsigned long long t0 = gtimer();
       while (!mbar_try(smem_u32(&sh.drain), 0) && gtimer() - t0 < PF_TIMEOUT_NS) {
-      }
-    } else {
-      // -------------------------------------------------------------- jobs ----
-      PfWalk walk;
-      walk.begin(p, blockIdx.x, lane);
-      for (uint32_t n = 0;; n++) {
-        const int i = n % PF_RECS;
-        bool ok = true;
-        if (n >= PF_RECS) ok = pf_wait(sh, &sh.rec_empty[i], n / PF_RECS - 1);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        if (lane == 0) {
-          PfRec r{};
-          r.b = -1;
-          if (walk.more) {
-            r.b = walk.job.s.b;
-            r.h = walk.job.h;
-            r.len = walk.job.s.len;
-            const int token = walk.job.j * p.tokens;
-            r.row = walk.job.s.first + token;
-            r.pos = walk.job.s.len - walk.job.s.n + token;
-            r.ka = walk.ka;
-            for (int t = 0; t < 2; t++) {
-              r.rows[t] = walk.rows(p, t);
-              r.e[t] = walk.end_of(p, t);
-            }
-            r.whole = walk.whole;
-            r.slot = walk.first ? 0 : 1;
-          }
-          sh.rec[i] = r;
-          mbar_arrive(smem_u32(&sh.rec_full[i]));
-        }
-        __syncwarp();
-        if (!walk.more) break;
-        walk.next(p);
       }
     }
   } else {
@@ -714,37 +860,17 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
     const uint32_t s_addr = tmem + lane_base + Sh::S_COL + 128 * t;
     const uint32_t o_addr = tmem + lane_base + Sh::O_COL + D * t;
     const uint32_t p_addr = SEP ? tmem + lane_base + Sh::P_COL + 64 * t : s_addr;
-    const int row = 128 * t + r, row_token = row / a.G, row_head = row % a.G;
-    uint32_t taken = 0, sp = 0, vp = 0;  // records taken; phases of s_full and pv_done
+    const int row = 128 * t + r, row_token = t * (p.tokens / 2) + r / a.G, row_head = r % a.G;
+    uint32_t taken = 0, tiles = 0, sp = 0, vp = 0;  // records, tiles; phases of s_full and pv_done
     bool ok = true;
-    PfRec w, nx;
-    // A job's row of queries, one per thread, into the swizzled tile.  The tile is
-    // free as soon as the last S of the job before is there.
-    auto load_q = [&](const PfRec& x) {
-      const bool in = r < (t == 0 ? x.rows[0] : x.rows[1]);
-      const uint16_t* src = (const uint16_t*)a.q.p;
-      if (in) src += (x.row + row_token) * a.q.ts + ((long long)x.h * a.G + row_head) * a.q.hs;
-      const uint32_t dst = q_smem + t * Sh::TILE + r * 128;
-#pragma unroll
-      for (int k = 0; k < D / 8; k++)
-        cp_async16_zfill(dst + (k >> 3) * 16384 + (((k ^ r) & 7) << 4), src + (in ? 8 * k : 0), in);
-    };
-    auto units = [&](const PfRec& x) { return (t == 0 ? x.e[0] : x.e[1]) - x.ka; };
-    bool more = pf_take(sh, taken, w, lane == 0);
-    if (more && units(w) > 0) load_q(w);
-    while (more) {
+    PfRec w;
+    while (ok && pf_take(sh, taken, w, lane == 0)) {
       const int rows = t == 0 ? w.rows[0] : w.rows[1];
-      const int ka = w.ka, kb = ka + units(w);
-      nx.b = -1;
+      const int ka = w.ka, kb = t == 0 ? w.e[0] : w.e[1];
+      if (rows <= 0) continue;
       // the last cache row this row sees (rows that do not exist: every one)
       const int last = r < rows ? w.pos + row_token : 0x3FFFFFFF;
       float m = -INFINITY, l = 0.f;
-      if (kb > ka) {
-        cp_async_wait_all();
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[t]));
-      }
       for (int j = ka; j < kb; j++) {
         ok = __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.s_full[t], sp));
         if (!ok) break;
@@ -752,40 +878,42 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
         tc_fence_after();
         uint32_t x[128];
         tmem_ld64(s_addr, x);
+        // (the maximum of the first half while the second half comes)
+        tmem_ld64_wait(x);
         tmem_ld64(s_addr + 64, x + 64);
+        // columns 0 .. limit count; of a 32-column block some, or none (dead), may not
+        const int limit = last - j * PF_UNIT;
+        mask32(x, limit);
+        mask32(x + 32, limit - 32);
+        const float mx_a = max64(x);
+        tmem_ld64_wait(x + 64);
         if (SEP) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.s_free[t]));
         }
-        const int limit = last - j * PF_UNIT;  // columns 0 .. limit count
-        if (__any_sync(0xFFFFFFFFu, limit < PF_UNIT - 1)) {
-#pragma unroll
-          for (int i = 0; i < 128; i++)
-            if (i > limit) x[i] = 0xFF800000u;  // -inf
-        }
-        float mx0 = __uint_as_float(x[0]), mx1 = __uint_as_float(x[1]);
-#pragma unroll
-        for (int i = 2; i < 126; i += 4) {
-          mx0 = max3(mx0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-          mx1 = max3(mx1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
-        }
-        const float mx = max3(fmaxf(mx0, mx1), __uint_as_float(x[126]), __uint_as_float(x[127])) * p.scale2;
+        mask32(x + 64, limit - 64);
+        mask32(x + 96, limit - 96);
+        const float mx = fmaxf(mx_a, max64(x + 64)) * p.scale2;
+        const bool higher = mx > m + 8.f, raise = __any_sync(0xFFFFFFFFu, higher);
         // O and P are this thread's to write once the product before is done (where
         // P takes S's place, this S is the sign of it)
-        const bool higher = mx > m + 8.f, raise = __any_sync(0xFFFFFFFFu, higher);
-        if (SEP && j > ka) {
+        bool waited = !(SEP && j > ka);
+        auto pv_wait = [&]() {
+          if (waited) return;
+          waited = true;
           ok = __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.pv_done[t], vp));
-          if (!ok) break;
           vp ^= 1;
           tc_fence_after();
-        }
+        };
         if (raise) {
           // (each row by its own scores alone, so that no row's bits depend on another)
           const float f = higher ? join_weight(m, mx) : 1.f;
           if (higher) m = mx;
           l *= f;
           if (j > ka) {
+            pv_wait();
+            if (!ok) break;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t y[32];
@@ -798,7 +926,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
         }
         const float neg = m == -INFINITY ? 0.f : -m;
         const float2 sc = make_float2(p.scale2, p.scale2), ng = make_float2(neg, neg);
-        float2 sum = make_float2(0.f, 0.f);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int half = 0; half < 2; half++) {
           uint32_t y[32];
@@ -808,23 +936,25 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
             float2 e = ffma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), sc, ng);
             e.x = ex2(e.x);
             e.y = ex2(e.y);
-            sum = fadd2(sum, e);
+            sum[i & 1] = fadd2(sum[i & 1], e);
             y[i] = bf2(e.x, e.y);
           }
-          tmem_st32(p_addr + 32 * half, y);
-        }
-        l += sum.x + sum.y;
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[t]));
-        if (j == kb - 1) {  // while the last product runs: the next job's queries
-          if (pf_take(sh, taken, nx, lane == 0)) {
-            if (units(nx) > 0) load_q(nx);
-          } else {
-            nx.b = -2;
+          if (half == 0) {
+            pv_wait();
+            if (!ok) break;
           }
+          tmem_st32(p_addr + 32 * half, y);
+          if (SEP && half == 0) {
+            if (threadIdx.x == 128) sh.progress = ++tiles;
+            continue;
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(half == 0 ? &sh.p_half[t] : &sh.p_full[t]));
         }
+        if (!ok) break;
+        l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
       }
       if (!ok) break;
       // -- the job's end: out = o / l, or a partial state
@@ -843,23 +973,30 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
       float bad = 0.f;
       if (kb > ka) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t y[32];
-          tmem_ld32(o_addr + c, y);
+        for (int c = 0; c < D; c += 64) {
+          uint32_t y[64];
+          tmem_ld64(o_addr + c, y);
+          tmem_ld64_wait(y);
+          float b[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 32; i++) bad = fmaf(__uint_as_float(y[i]), 0.f, bad);
+          for (int i = 0; i < 64; i++) b[i & 3] = fmaf(__uint_as_float(y[i]), 0.f, b[i & 3]);
+          bad += (b[0] + b[1]) + (b[2] + b[3]);
           if (mine && w.whole) {
+            const float2 f = make_float2(inv, inv), zero = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              float f[8];
+            for (int i = 0; i < 64; i += 8) {
+              uint32_t z[4];
 #pragma unroll
-              for (int e = 0; e < 8; e++) f[e] = l == 0.f ? 0.f : __uint_as_float(y[i + e]) * inv;
-              *(uint4*)(out + c + i) = make_uint4(bf2(f[0], f[1]), bf2(f[2], f[3]), bf2(f[4], f[5]),
-                                                  bf2(f[6], f[7]));
+              for (int e = 0; e < 4; e++) {
+                const float2 v = ffma2(make_float2(__uint_as_float(y[i + 2 * e]),
+                                                   __uint_as_float(y[i + 2 * e + 1])), f, zero);
+                z[e] = bf2(v.x, v.y);
+              }
+              *(uint4*)(out + c + i) = make_uint4(z[0], z[1], z[2], z[3]);
             }
           } else if (mine) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
+            for (int i = 0; i < 64; i += 4)
               *(uint4*)(st + ((size_t)(c + i) / 4 * PF_ROWS + row) * 4) =
                   make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
           }
@@ -887,8 +1024,8 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
         redo &= redo - 1;
         const int rr = __shfl_sync(0xFFFFFFFFu, row, src);
         const int end = __shfl_sync(0xFFFFFFFFu, last, src) + 1;
-        const int hh = w.h * a.G + rr % a.G;
-        const long long row_tok = w.row + rr / a.G;
+        const int hh = w.h * a.G + __shfl_sync(0xFFFFFFFFu, row_head, src);
+        const long long row_tok = w.row + __shfl_sync(0xFFFFFFFFu, row_token, src);
         float m1, l1, o1[D / 32];
         attn_row<D>(a.kv, w.b, w.h, (const uint16_t*)a.q.p + row_tok * a.q.ts + hh * a.q.hs,
                     a.scale, ka * PF_UNIT, min(end, kb * PF_UNIT), m1, l1, o1);
@@ -904,14 +1041,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
             st[((size_t)(dim / 4) * PF_ROWS + rr) * 4 + dim % 4] = o1[e] * f1;
         }
       }
-      if (kb == ka) {
-        if (!pf_take(sh, taken, nx, lane == 0)) nx.b = -2;
-        else if (units(nx) > 0) load_q(nx);
-      }
-      more = nx.b >= 0;
-      w = nx;
     }
-    cp_async_wait_all();
   }
   __syncwarp();
   tc_fence_before();
@@ -920,74 +1050,56 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Block (x, y): if cut x + 1 of the line is the first inside its job, joins rows
-// [32 y, 32 y + 32) of that job's parts.  A warp has 32 rows, one per lane, and
-// an eighth of the head's dimensions.
+// Block (x, y): if part x + 1 is the first to begin inside its job, joins rows
+// [32 y, 32 y + 32) of that job's parts: the last job of part x, then the first
+// jobs of the parts from x + 1 on that begin inside the same job.  A warp has 32
+// rows, one per lane, and an eighth of the head's dimensions.
 template <int D>
 __global__ void __launch_bounds__(256) kv_prefill_join_kernel(const __grid_constant__ PfArgs p, int blocks) {
   using Sh = PfShape<D>;
   constexpr int N = D / 32;  // float4 pieces per warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int i = blockIdx.x + 1;
   const AttnArgs& a = p.a;
-  const PfSeq s0 = pf_seq(p, lane);
-  const PfLine line = pf_line(p, blocks, lane, s0);
-  bool mine = i < line.parts;
-  PfCut cut{};
-  int slot = 0;
-  if (mine) {
-    const PfCut both = pf_find(p, line.begin(i - 1), line.begin(i), line.snap, lane, s0);
-    const PfCut prev = pf_shfl(both, 0);
-    cut = pf_shfl(both, 1);
-    const bool inside = cut.unit > 0 && cut.unit < PF_AFTER;
-    const bool same = pf_same(prev.job, cut.job);
-    mine = inside && !(same && prev.unit > 0 && prev.unit < PF_AFTER);
-    if (mine) {  // slot 0: the job is the first one of block i - 1
-      PfJob start = prev.job;
-      if (prev.unit == PF_AFTER) pf_next(p, start);
-      const bool whole_start = prev.unit == PF_AFTER || prev.unit == 0;
-      slot = whole_start && pf_same(start, cut.job) ? 0 : 1;
-    }
-  }
+  const PfPart* parts = (const PfPart*)(a.ws + (size_t)blocks * 2 * Sh::STATE);
+  const int i = blockIdx.x + 1;
   pdl_wait();
-  if (!mine) return;
-  const int row = 32 * blockIdx.y + lane;
-  const int n_rows = min(p.tokens, cut.job.s.n - cut.job.j * p.tokens) * a.G;
-  const bool live = row < n_rows;
-  const long long start = line.begin(i) - cut.off;  // of the job on the line
+  const PfPart job = parts[i], prev = parts[i - 1];
+  auto same = [&](const PfPart& x) { return x.b == job.b && x.h == job.h && x.j == job.j; };
+  if (!job.inside || (prev.inside && same(prev))) return;
+  const int row = 32 * blockIdx.y + lane, tile = row >> 7, r = row & 127;
+  const bool live = r < job.rows[tile];
   float m = -INFINITY, l = 0.f;
   float4 o[N];
 #pragma unroll
   for (int c = 0; c < N; c++) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const long long size = pf_before(p, cut.job.s, cut.job.j + 1) - pf_before(p, cut.job.s, cut.job.j);
-  int unit = 0;  // where the part begins
-  for (int k = i - 1;; k++) {
-    // part k ends at cut k + 1
-    const long long off = line.begin(k + 1) - start;
-    const int until = k + 1 >= line.parts || off >= size ? PF_AFTER : pf_unit_at(p, cut.job, off, line.snap);
-    if (until > unit && live) {
-      const float* st = a.ws + ((size_t)k * 2 + (k == i - 1 ? slot : 0)) * Sh::STATE;
-      const float mi = st[PF_ROWS * D + row], li = st[PF_ROWS * D + PF_ROWS + row];
-      if (!(li == 0.f)) {
-        const float top = fmaxf(m, mi), f = join_weight(m, top), g = join_weight(mi, top);
-        m = top;
-        l = l * f + li * g;
-#pragma unroll
-        for (int c = 0; c < N; c++) {
-          const float4 y = *(const float4*)(st + ((size_t)(warp * N + c) * PF_ROWS + row) * 4);
-          o[c].x = o[c].x * f + y.x * g;
-          o[c].y = o[c].y * f + y.y * g;
-          o[c].z = o[c].z * f + y.z * g;
-          o[c].w = o[c].w * f + y.w * g;
-        }
-      }
+  for (int k = i - 1; k < blocks; k++) {
+    int slot = 0;
+    if (k == i - 1) {
+      slot = prev.more && same(prev) ? 0 : 1;  // (the job may be that part's first one, too)
+    } else {
+      const PfPart x = parts[k];
+      if (!x.inside || !same(x)) break;
+      if (!x.more) continue;
     }
-    if (until == PF_AFTER) break;
-    unit = until;
+    if (!live) continue;
+    const float* st = a.ws + ((size_t)k * 2 + slot) * Sh::STATE;
+    const float mi = st[PF_ROWS * D + row], li = st[PF_ROWS * D + PF_ROWS + row];
+    if (li == 0.f) continue;  // no weight; o was not written
+    const float top = fmaxf(m, mi), f = join_weight(m, top), g = join_weight(mi, top);
+    m = top;
+    l = l * f + li * g;
+#pragma unroll
+    for (int c = 0; c < N; c++) {
+      const float4 y = *(const float4*)(st + ((size_t)(warp * N + c) * PF_ROWS + row) * 4);
+      o[c].x = o[c].x * f + y.x * g;
+      o[c].y = o[c].y * f + y.y * g;
+      o[c].z = o[c].z * f + y.z * g;
+      o[c].w = o[c].w * f + y.w * g;
+    }
   }
   if (!live) return;
-  const int token = cut.job.j * p.tokens + row / a.G, hq = cut.job.h * a.G + row % a.G;
-  const long long tok = cut.job.s.first + token;
+  const int hq = job.h * a.G + r % a.G;
+  const long long tok = job.row + tile * (p.tokens / 2) + r / a.G;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint16_t* out = (uint16_t*)a.o.p + tok * a.o.ts + hq * a.o.hs + warp * N * 4;
 #pragma unroll

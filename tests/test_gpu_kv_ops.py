@@ -567,3 +567,40 @@ def test_shared_prefix_blocks():
     c.table[1, :4] = c.table[0, :4]
     c.check("decode", c.run("decode"))
     c.check("prefill", c.run("prefill"))
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+def test_query_orders(kind):
+    # queries with heads first in memory, and one row shared by all heads
+    c = Case((6, 3, 64), [200, 90, 33], [1, 1, 1], block=16, seed=28)
+    plain, plain_lse = c.run(kind)
+    c.q = c.q.transpose(0, 1).contiguous().transpose(0, 1)
+    got, lse = c.run(kind)
+    assert torch.equal(got, plain) and torch.equal(lse, plain_lse)
+    c.q = c.q[:, :1].expand(-1, 6, -1)
+    assert c.q.stride(1) == 0
+    c.check(kind, c.run(kind))
+    c = Case((1, 1, 128), [40], [1], block=0, seed=29)  # a single row
+    c.check(kind, c.run(kind))
+
+
+def test_attention_workspace_is_checked():
+    from decode_megakernel_sm_gb300 import _lib as L
+    c = Case((4, 2, 64), [40, 20], [1, 1], block=16, seed=30)
+    view = L.mk_kv_view(c.k.data_ptr(), c.v.data_ptr(), *c.k.shape, c.table.data_ptr(),
+                        c.table.shape[1])
+    rows = L.mk_rows(c.q.data_ptr(), 256, 64)
+    out = torch.empty_like(c.q)
+    to = L.mk_rows(out.data_ptr(), 256, 64)
+    for decode, f, cu in ((True, L.mk_attn_decode, None), (False, L.mk_attn_prefill, c.cu.data_ptr())):
+        need = L.mk_attn_workspace_bytes(decode, 2, 2, 4, 2, 64)
+        assert need > 0
+        ws = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+        bt = L.mk_kv_batch(2, 2, c.lens.data_ptr(), cu)
+        for p, n in ((None, need), (ws.data_ptr(), need - 1), (ws.data_ptr() + 16, need)):
+            with pytest.raises(MkError) as e:
+                f(view, bt, 4, rows, 0.125, to, None, p, n)
+            assert e.value.status == MK_ERR_INVALID_ARG
+        f(view, bt, 4, rows, 0.125, to, None, ws.data_ptr(), need)
+        ref, _, A, err = c.reference(0.125)
+        assert ((out.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -7 * A).all()
