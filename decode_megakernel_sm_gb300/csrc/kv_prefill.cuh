@@ -60,7 +60,9 @@ constexpr int PF_ROWS = 256;      // rows of a job
 constexpr int PF_UNIT = 128;      // cache rows of a unit
 constexpr int PF_JOB_COST = 256;  // a job's start and end, in keys
 constexpr int PF_MIN_SHARE = 4 * PF_UNIT;  // a part of a job is not worth less
-constexpr int PF_SNAP = 16;       // a cut this part of a share from a job's border moves there
+// A cut this part of a share, or these keys, from a job's border moves there: a
+// partial state and its join cost about as much.
+constexpr int PF_SNAP = 16, PF_SNAP_KEYS = 4 * PF_UNIT;
 constexpr int PF_STAGGER = 2000;  // cycles
 constexpr int PF_AFTER = 1 << 30;
 constexpr unsigned long long PF_TIMEOUT_NS = 2000000000ull;
@@ -158,7 +160,7 @@ MK_DEV PfLine pf_line(const PfArgs& p, int blocks, int lane, const PfSeq& s0) {
   if (l.parts > 0) {
     l.quot = l.total / l.parts;
     l.rest = (int)(l.total - l.quot * l.parts);
-    l.snap = l.quot / PF_SNAP;
+    l.snap = max(l.quot / PF_SNAP, (long long)PF_SNAP_KEYS);
   }
   return l;
 }
@@ -1068,34 +1070,58 @@ __global__ void __launch_bounds__(256) kv_prefill_join_kernel(const __grid_const
   if (!job.inside || (prev.inside && same(prev))) return;
   const int row = 32 * blockIdx.y + lane, tile = row >> 7, r = row & 127;
   const bool live = r < job.rows[tile];
+  // The parts behind part i - 1, 32 at a time: how many begin inside the job, and
+  // which of them hold anything.
   float m = -INFINITY, l = 0.f;
   float4 o[N];
 #pragma unroll
   for (int c = 0; c < N; c++) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = i - 1; k < blocks; k++) {
-    int slot = 0;
-    if (k == i - 1) {
-      slot = prev.more && same(prev) ? 0 : 1;  // (the job may be that part's first one, too)
-    } else {
-      const PfPart x = parts[k];
-      if (!x.inside || !same(x)) break;
-      if (!x.more) continue;
-    }
-    if (!live) continue;
-    const float* st = a.ws + ((size_t)k * 2 + slot) * Sh::STATE;
-    const float mi = st[PF_ROWS * D + row], li = st[PF_ROWS * D + PF_ROWS + row];
-    if (li == 0.f) continue;  // no weight; o was not written
-    const float top = fmaxf(m, mi), f = join_weight(m, top), g = join_weight(mi, top);
-    m = top;
-    l = l * f + li * g;
+  // Joins the states of up to four parts k0 + (bits of mask), all loads in flight at
+  // once; slot: of the first part's state.
+  auto join = [&](int k0, unsigned mask, int slot) {
+    while (mask) {
+      float mi[4], li[4];
+      float4 y[4][N];
 #pragma unroll
-    for (int c = 0; c < N; c++) {
-      const float4 y = *(const float4*)(st + ((size_t)(warp * N + c) * PF_ROWS + row) * 4);
-      o[c].x = o[c].x * f + y.x * g;
-      o[c].y = o[c].y * f + y.y * g;
-      o[c].z = o[c].z * f + y.z * g;
-      o[c].w = o[c].w * f + y.w * g;
+      for (int n = 0; n < 4; n++) {
+        const bool in = mask != 0 && live;
+        const int k = k0 + (mask ? __ffs(mask) - 1 : 0);
+        mask &= mask - 1;
+        const float* st = a.ws + ((size_t)k * 2 + slot) * Sh::STATE;
+        mi[n] = in ? st[PF_ROWS * D + row] : -INFINITY;
+        li[n] = in ? st[PF_ROWS * D + PF_ROWS + row] : 0.f;
+#pragma unroll
+        for (int c = 0; c < N; c++)
+          y[n][c] = in ? *(const float4*)(st + ((size_t)(warp * N + c) * PF_ROWS + row) * 4)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int n = 0; n < 4; n++) {
+        if (li[n] == 0.f) continue;  // no weight; o was not written
+        const float top = fmaxf(m, mi[n]), f = join_weight(m, top), g = join_weight(mi[n], top);
+        m = top;
+        l = l * f + li[n] * g;
+#pragma unroll
+        for (int c = 0; c < N; c++) {
+          o[c].x = o[c].x * f + y[n][c].x * g;
+          o[c].y = o[c].y * f + y[n][c].y * g;
+          o[c].z = o[c].z * f + y[n][c].z * g;
+          o[c].w = o[c].w * f + y[n][c].w * g;
+        }
+      }
     }
+  };
+  // (the job may be the first one of part i - 1, too)
+  join(i - 1, 1u, prev.more && same(prev) ? 0 : 1);
+  for (int k0 = i; k0 < blocks; k0 += 32) {
+    PfPart x{};
+    x.b = -1;
+    if (k0 + lane < blocks) x = parts[k0 + lane];
+    const unsigned ours = __ballot_sync(0xFFFFFFFFu, x.b >= 0 && x.inside && same(x));
+    const unsigned more = __ballot_sync(0xFFFFFFFFu, x.more);
+    const unsigned run = ours == 0xFFFFFFFFu ? ours : (1u << __ffs(~ours) - 1) - 1;  // up to the first that is not
+    join(k0, run & more, 0);
+    if (run != 0xFFFFFFFFu) break;
   }
   if (!live) return;
   const int hq = job.h * a.G + r % a.G;
