@@ -60,10 +60,9 @@ constexpr int PF_ROWS = 256;      // rows of a job
 constexpr int PF_UNIT = 128;      // cache rows of a unit
 constexpr int PF_JOB_COST = 256;  // a job's start and end, in keys
 constexpr int PF_MIN_SHARE = 4 * PF_UNIT;  // a part of a job is not worth less
-// A cut this part of a share, or these keys, from a job's border moves there: a
-// partial state and its join cost about as much.
-constexpr int PF_SNAP = 16, PF_SNAP_KEYS = 4 * PF_UNIT;
-constexpr int PF_STAGGER = 2000;  // cycles
+// A cut so many keys from a job's border moves there: a partial state and its join
+// cost about as much.
+constexpr int PF_SNAP = 4 * PF_UNIT;
 constexpr int PF_AFTER = 1 << 30;
 constexpr unsigned long long PF_TIMEOUT_NS = 2000000000ull;
 
@@ -136,7 +135,6 @@ MK_DEV int pf_units(const PfArgs& p, const PfJob& w) {
 struct PfLine {
   long long total, quot;
   int parts, rest;
-  long long snap;  // a cut this near to a job's border moves there
   MK_DEV long long begin(int i) const { return quot * i + (unsigned)rest * (unsigned)i / (unsigned)parts; }
 };
 
@@ -160,17 +158,16 @@ MK_DEV PfLine pf_line(const PfArgs& p, int blocks, int lane, const PfSeq& s0) {
   if (l.parts > 0) {
     l.quot = l.total / l.parts;
     l.rest = (int)(l.total - l.quot * l.parts);
-    l.snap = max(l.quot / PF_SNAP, (long long)PF_SNAP_KEYS);
   }
   return l;
 }
 
 // Unit of a job at which a cut `off` keys from its start falls.
-MK_DEV int pf_unit_at(const PfArgs& p, const PfJob& w, long long off, long long snap) {
+MK_DEV int pf_unit_at(const PfArgs& p, const PfJob& w, long long off) {
   const int units = pf_units(p, w);
   const long long size = pf_before(p, w.s, w.j + 1) - pf_before(p, w.s, w.j);
-  if (off <= snap) return off == 0 || off < size - off ? 0 : PF_AFTER;
-  if (size - off <= snap) return PF_AFTER;
+  if (off <= PF_SNAP) return off == 0 || off < size - off ? 0 : PF_AFTER;
+  if (size - off <= PF_SNAP) return PF_AFTER;
   const long long u = (off + PF_UNIT / 2) / PF_UNIT;
   return u >= units ? PF_AFTER : (int)u;
 }
@@ -178,7 +175,7 @@ MK_DEV int pf_unit_at(const PfArgs& p, const PfJob& w, long long off, long long 
 // Where cut c (keys from the start) falls; from the total on, the end of the
 // line (one warp, c the same or not on its lanes as `c0` for the even and `c1`
 // for the odd ones: two cuts for the price of one).
-MK_DEV PfCut pf_find(const PfArgs& p, long long c0, long long c1, long long snap, int lane, const PfSeq& s0) {
+MK_DEV PfCut pf_find(const PfArgs& p, long long c0, long long c1, int lane, const PfSeq& s0) {
   long long before = 0;
   PfCut r{};
   r.job.s.b = p.a.bt.batch;
@@ -228,7 +225,7 @@ MK_DEV PfCut pf_find(const PfArgs& p, long long c0, long long c1, long long snap
     while (j + 1 < q.jobs && pf_before(p, q, j + 1) <= rem) j++;
     r.job.j = j;
     r.off = rem - pf_before(p, q, j);
-    r.unit = pf_unit_at(p, r.job, r.off, snap);
+    r.unit = pf_unit_at(p, r.job, r.off);
   }
   return r;
 }
@@ -287,7 +284,7 @@ struct PfWalk {
     more = inside = false;
     job.s.b = -1;
     if (part >= line.parts) return;
-    const PfCut both = pf_find(p, line.begin(part), line.begin(part + 1), line.snap, lane, s0);
+    const PfCut both = pf_find(p, line.begin(part), line.begin(part + 1), lane, s0);
     const PfCut c = pf_shfl(both, 0);
     end = pf_shfl(both, 1);
     job = c.job;
@@ -375,7 +372,6 @@ struct PfShared {
   PfRec rec[PF_RECS];
   uint32_t tmem;
   volatile int abort;
-  volatile uint32_t progress;  // S tiles that tile 0's softmax has half done
 };
 
 // Wait for phase `n` (counted from 0) of a barrier; false if the block gave up.
@@ -486,6 +482,15 @@ MK_DEV void tmem_ld32(uint32_t addr, uint32_t* x) {
       : "r"(addr)
       : "memory");
 }
+template <int N>
+MK_DEV void tmem_ldn(uint32_t addr, uint32_t* x) {
+  if (N == 64) {
+    tmem_ld64(addr, x);
+    tmem_ld64_wait(x);
+  } else {
+    tmem_ld32(addr, x);
+  }
+}
 MK_DEV void tmem_st32(uint32_t addr, const uint32_t* x) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -513,15 +518,6 @@ MK_DEV float max64(const uint32_t* x) {
       m[c] = max3(m[c], __uint_as_float(x[i + c]), __uint_as_float(x[i + c + 4]));
   }
   return max3(fmaxf(m[0], m[1]), m[2], m[3]);
-}
-
-// -inf in the places behind `limit` (one warp: nothing to do where no lane's
-// limit is below the last).
-MK_DEV void mask32(uint32_t* x, int limit) {
-  if (!__any_sync(0xFFFFFFFFu, limit < 31)) return;
-#pragma unroll
-  for (int i = 0; i < 32; i++)
-    if (i > limit) x[i] = 0xFF800000u;
 }
 
 // 2^x to about 2 units in the last place; results below 2^-126 are zero.
@@ -574,7 +570,6 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
     }
     mbar_init(smem_u32(&sh.drain), 2);
     sh.abort = 0;
-    sh.progress = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), 512);
@@ -668,13 +663,17 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
           const int row = j * PF_UNIT, left = w.len - row;
           if (is_v && left < PF_UNIT) {
             // the end of the sequence: zeros behind it
-            for (int c = lane; c < PF_UNIT * (D / 8); c += 32) {
-              const int r = c / (D / 8), k = c % (D / 8);
-              long long src = -1;
-              if (r < left) src = kv_row_of(a.kv, w.b, w.h, row + r);
+            const int k = lane % (D / 8);  // 16-byte chunk of a row
+#pragma unroll 4
+            for (int r = lane / (D / 8); r < PF_UNIT; r += 32 / (D / 8)) {
+              const int b = __shfl_sync(0xFFFFFFFFu, blk, r / p.box);
+              const bool in = r < left && (unsigned)b < (unsigned)a.kv.n_blocks;
+              const long long src = ((long long)b * a.kv.Hkv + w.h) * a.kv.block + ((row + r) & in_block);
               cp_async16_zfill(dst + (k >> 3) * 16384 + r * 128 + (((k ^ r) & 7) << 4),
-                               src < 0 ? a.kv.v : a.kv.v + src * D + k * 8, src >= 0);
+                               in ? a.kv.v + src * D + k * 8 : a.kv.v, in);
             }
+            if (__any_sync(0xFFFFFFFFu, (int)my_box < left && (unsigned)blk >= (unsigned)a.kv.n_blocks))
+              kv_fail(MK_ERR_INVALID_ARG);
             cp_async_wait_all();
             fence_async_smem();
             __syncwarp();
@@ -723,7 +722,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
       // by tile, bit t: phases of s_free, p_half / p_full, q_full, o_empty; whether
       // an S, an O has been made
       uint32_t ph_s = 0, ph_p = 0, ph_q = 0, ph_o = 0, any_s = 0, any_o = 0;
-      uint32_t taken = 0, tiles0 = 0;  // records taken, S tiles that tile 0 had before
+      uint32_t taken = 0;  // records
       bool ok = true;
       PfRec w;
       auto wait = [&](const unsigned long long* bar, uint32_t phase) {
@@ -790,34 +789,36 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
       if (SEP) {
         // 64-dim heads, a warp per tile: the exponentials bound them, and neither
         // tile's softmax may wait for the other's
+        // (the S of a unit, of the next job if need be, comes before the P of the one
+        // before it)
         const int t = warp >> 1;
-        while (ok && pf_take(sh, taken, w, lane == 0)) {
+        auto s_of = [&](int j, int ka, int e) {
+          if (j == ka && j < e) wait_tile(sh.q_full, ph_q, t);
+          k_wait();
+          if (j < e) qk(t, j + 1 == e);
+          k_next();
+        };
+        auto take = [&]() {  // the next job with anything to do
+          bool got;
+          do {
+            got = pf_take(sh, taken, w, lane == 0);
+          } while (got && w.ka == max(w.e[0], w.e[1]));
+          return got;
+        };
+        bool more = take();
+        if (more) s_of(w.ka, w.ka, t == 0 ? w.e[0] : w.e[1]);
+        while (more && ok) {
           const int ka = w.ka, e = t == 0 ? w.e[0] : w.e[1], kb = max(w.e[0], w.e[1]);
-          if (ka == kb) continue;
-          if (ka < e) {
-            wait_tile(sh.q_full, ph_q, t);
-            // Tile 1 starts half a step behind tile 0, so that one's exponentials run
-            // beside the other's maxima and products; side by side they would stay
-            // side by side.  (A hint: it waits a microsecond at most.)
-            if (t == 1 && ka < w.e[0]) {
-              const long long t0 = clock64();
-              while ((int)(sh.progress - (tiles0 + 1)) < 0 && clock64() - t0 < PF_STAGGER) {
-              }
-              __syncwarp();
-            }
-          }
-          tiles0 += w.e[0] - ka;
-          for (int j = ka - 1; j < kb && ok; j++) {
+          for (int j = ka; j < kb && ok; j++) {
             if (j + 1 < kb) {
-              k_wait();
-              if (j + 1 < e) qk(t, j + 2 == e);
-              k_next();
+              s_of(j + 1, ka, e);
+            } else {
+              more = take();
+              if (more) s_of(w.ka, w.ka, t == 0 ? w.e[0] : w.e[1]);
             }
-            if (j >= ka) {
-              wait(&sh.v_full[vs], vp);
-              if (j < e) pv(t, j == ka, j + 1 == e);
-              v_next();
-            }
+            wait(&sh.v_full[vs], vp);
+            if (j < e) pv(t, j == ka, j + 1 == e);
+            v_next();
           }
         }
       } else if (warp == 1) {
@@ -863,7 +864,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
     const uint32_t o_addr = tmem + lane_base + Sh::O_COL + D * t;
     const uint32_t p_addr = SEP ? tmem + lane_base + Sh::P_COL + 64 * t : s_addr;
     const int row = 128 * t + r, row_token = t * (p.tokens / 2) + r / a.G, row_head = r % a.G;
-    uint32_t taken = 0, tiles = 0, sp = 0, vp = 0;  // records, tiles; phases of s_full and pv_done
+    uint32_t taken = 0, sp = 0, vp = 0;  // records; phases of s_full and pv_done
     bool ok = true;
     PfRec w;
     while (ok && pf_take(sh, taken, w, lane == 0)) {
@@ -878,15 +879,28 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
         if (!ok) break;
         sp ^= 1;
         tc_fence_after();
+        const int limit = last - j * PF_UNIT;  // columns 0 .. limit count
+        // A job's last units are masked in tensor memory, in a small loop: selects on
+        // the registers of S cost every unit a tenth of its time, and a copy of the
+        // unit for them costs every job its instruction fetches.
+        if (__any_sync(0xFFFFFFFFu, limit < PF_UNIT - 1)) {
+#pragma unroll 1
+          for (int c = 0; c < PF_UNIT; c += 32) {
+            if (!__any_sync(0xFFFFFFFFu, limit < c + 31)) continue;
+            uint32_t y[32];
+            tmem_ld32(s_addr + c, y);
+#pragma unroll
+            for (int i = 0; i < 32; i++)
+              if (c + i > limit) y[i] = 0xFF800000u;  // -inf
+            tmem_st32(s_addr + c, y);
+          }
+          tmem_st_wait();
+        }
         uint32_t x[128];
         tmem_ld64(s_addr, x);
         // (the maximum of the first half while the second half comes)
         tmem_ld64_wait(x);
         tmem_ld64(s_addr + 64, x + 64);
-        // columns 0 .. limit count; of a 32-column block some, or none (dead), may not
-        const int limit = last - j * PF_UNIT;
-        mask32(x, limit);
-        mask32(x + 32, limit - 32);
         const float mx_a = max64(x);
         tmem_ld64_wait(x + 64);
         if (SEP) {
@@ -894,28 +908,22 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.s_free[t]));
         }
-        mask32(x + 64, limit - 64);
-        mask32(x + 96, limit - 96);
         const float mx = fmaxf(mx_a, max64(x + 64)) * p.scale2;
         const bool higher = mx > m + 8.f, raise = __any_sync(0xFFFFFFFFu, higher);
         // O and P are this thread's to write once the product before is done (where
         // P takes S's place, this S is the sign of it)
-        bool waited = !(SEP && j > ka);
-        auto pv_wait = [&]() {
-          if (waited) return;
-          waited = true;
+        if (SEP && j > ka) {
           ok = __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.pv_done[t], vp));
+          if (!ok) break;
           vp ^= 1;
           tc_fence_after();
-        };
+        }
         if (raise) {
           // (each row by its own scores alone, so that no row's bits depend on another)
           const float f = higher ? join_weight(m, mx) : 1.f;
           if (higher) m = mx;
           l *= f;
           if (j > ka) {
-            pv_wait();
-            if (!ok) break;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t y[32];
@@ -941,21 +949,13 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
             sum[i & 1] = fadd2(sum[i & 1], e);
             y[i] = bf2(e.x, e.y);
           }
-          if (half == 0) {
-            pv_wait();
-            if (!ok) break;
-          }
           tmem_st32(p_addr + 32 * half, y);
-          if (SEP && half == 0) {
-            if (threadIdx.x == 128) sh.progress = ++tiles;
-            continue;
-          }
+          if (SEP && half == 0) continue;
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(half == 0 ? &sh.p_half[t] : &sh.p_full[t]));
         }
-        if (!ok) break;
         l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
       }
       if (!ok) break;
@@ -972,21 +972,21 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
       float* st = a.ws + ((size_t)blockIdx.x * 2 + w.slot) * Sh::STATE;
       uint16_t* out = (uint16_t*)a.o.p + tok * a.o.ts + hq * a.o.hs;
       const float inv = l == 0.f ? 0.f : 1.f / l;
+      constexpr int N = D == 64 ? 64 : 32;  // columns at a time (shorter code, 2 % of the whole)
       float bad = 0.f;
       if (kb > ka) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 64) {
-          uint32_t y[64];
-          tmem_ld64(o_addr + c, y);
-          tmem_ld64_wait(y);
+        for (int c = 0; c < D; c += N) {
+          uint32_t y[N];
+          tmem_ldn<N>(o_addr + c, y);
           float b[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 64; i++) b[i & 3] = fmaf(__uint_as_float(y[i]), 0.f, b[i & 3]);
+          for (int i = 0; i < N; i++) b[i & 3] = fmaf(__uint_as_float(y[i]), 0.f, b[i & 3]);
           bad += (b[0] + b[1]) + (b[2] + b[3]);
           if (mine && w.whole) {
             const float2 f = make_float2(inv, inv), zero = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < 64; i += 8) {
+            for (int i = 0; i < N; i += 8) {
               uint32_t z[4];
 #pragma unroll
               for (int e = 0; e < 4; e++) {
@@ -998,7 +998,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
             }
           } else if (mine) {
 #pragma unroll
-            for (int i = 0; i < 64; i += 4)
+            for (int i = 0; i < N; i += 4)
               *(uint4*)(st + ((size_t)(c + i) / 4 * PF_ROWS + row) * 4) =
                   make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
           }
