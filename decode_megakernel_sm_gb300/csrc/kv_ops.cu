@@ -102,7 +102,7 @@ static int prefill_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
   if (rows >= 0x7FFFFFFFll) return MK_ERR_UNSUPPORTED;
   PfArgs p{};
   p.a = a;
-  p.tokens = PF_ROWS / 2 / a.G * 2;
+  p.per = PF_ROWS / 2 / a.G;
   p.negate = a.scale < 0.f;
   // (a scale of zero: so small that every finite score rounds to the same weight)
   p.scale2 = std::fmax(std::fabs(a.scale) * LOG2E, 1e-30f);
@@ -118,7 +118,7 @@ static int prefill_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
   // queries: [token][head][D], boxes of a tile's tokens and one kv head's heads
   const cuuint64_t qdims[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)a.bt.n_tokens};
   const cuuint64_t qstrides[2] = {(cuuint64_t)(a.q.hs * 2), (cuuint64_t)(a.q.ts * 2)};
-  const cuuint32_t qbox[3] = {64, (cuuint32_t)a.G, (cuuint32_t)p.tokens / 2}, qes[3] = {1, 1, 1};
+  const cuuint32_t qbox[3] = {64, (cuuint32_t)a.G, (cuuint32_t)p.per}, qes[3] = {1, 1, 1};
   if (enc(&maps[2], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q.p, qdims, qstrides, qbox, qes,
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)

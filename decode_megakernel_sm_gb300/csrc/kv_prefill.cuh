@@ -58,7 +58,7 @@ constexpr int PF_THREADS = 384;
 constexpr int PF_REGS = 168;      // per thread at launch (setmaxnreg deals them out anew)
 constexpr int PF_ROWS = 256;      // rows of a job
 constexpr int PF_UNIT = 128;      // cache rows of a unit
-constexpr int PF_JOB_COST = 256;  // a job's start and end, in keys
+constexpr int PF_JOB_COST = 320;  // a job's start and end, in keys (measured: 2.3 to 2.6 units)
 constexpr int PF_MIN_SHARE = 4 * PF_UNIT;  // a part of a job is not worth less
 // A cut so many keys from a job's border moves there: a partial state and its join
 // cost about as much.
@@ -85,7 +85,7 @@ struct PfPart {
 
 struct PfArgs {
   AttnArgs a;
-  int tokens;    // per job (two tiles)
+  int per;       // tokens of a tile
   int negate;    // the scale is negative: scale2 is its magnitude, Q K^T is negated
   float scale2;  // |scale| log2 e
   int box;       // rows of a TMA box
@@ -114,7 +114,7 @@ MK_DEV PfSeq pf_seq(const PfArgs& p, int b) {
   if (b < p.a.bt.batch) {
     s.len = kv_len(p.a.kv, p.a.bt, b);
     kv_new_tokens(p.a.bt, b, s.first, s.n);
-    s.jobs = (s.n + p.tokens - 1) / p.tokens;
+    s.jobs = (s.n + 2 * p.per - 1) / (2 * p.per);
   }
   return s;
 }
@@ -122,13 +122,13 @@ MK_DEV PfSeq pf_seq(const PfArgs& p, int b) {
 // Keys before job j of one kv head.
 MK_DEV long long pf_before(const PfArgs& p, const PfSeq& s, int j) {
   const long long base = max(0, s.len - s.n) + PF_JOB_COST;
-  return base * j + (long long)p.tokens * j * (j + 1) / 2;
+  return base * j + (long long)p.per * j * (j + 1);
 }
 
 // Cache rows that the job's token range [.., last] sees, and its units.
 MK_DEV int pf_seen(const PfSeq& s, int token) { return max(0, s.len - s.n + token + 1); }
 MK_DEV int pf_units(const PfArgs& p, const PfJob& w) {
-  return (pf_seen(w.s, min(w.s.n, p.tokens * (w.j + 1)) - 1) + PF_UNIT - 1) / PF_UNIT;
+  return (pf_seen(w.s, min(w.s.n, 2 * p.per * (w.j + 1)) - 1) + PF_UNIT - 1) / PF_UNIT;
 }
 
 // How the line is cut: part i begins at quot * i + rest * i / parts.
@@ -218,8 +218,8 @@ MK_DEV PfCut pf_find(const PfArgs& p, long long c0, long long c1, int lane, cons
     while (one * (h + 1) <= rem) h++;
     rem -= one * h;
     r.job.h = h;
-    const float base = (float)(max(0, q.len - q.n) + PF_JOB_COST) + 0.5f * p.tokens;
-    int j = (int)((sqrtf(base * base + 2.f * p.tokens * (float)rem) - base) / p.tokens);
+    const float base = (float)(max(0, q.len - q.n) + PF_JOB_COST) + p.per;
+    int j = (int)((sqrtf(base * base + 4.f * p.per * (float)rem) - base) / (2 * p.per));
     j = min(max(j, 0), q.jobs - 1);
     while (j > 0 && pf_before(p, q, j) > rem) j--;
     while (j + 1 < q.jobs && pf_before(p, q, j + 1) <= rem) j++;
@@ -325,7 +325,7 @@ struct PfWalk {
     r.b = job.s.b;
     r.h = job.h;
     r.len = job.s.len;
-    const int token = job.j * p.tokens;
+    const int token = 2 * job.j * p.per;
     r.row = job.s.first + token;
     r.pos = job.s.len - job.s.n + token;
     r.ka = ka;
@@ -344,19 +344,18 @@ struct PfWalk {
     r.j = job.j;
     r.inside = inside;
     r.more = more;
-    r.row = job.s.first + job.j * p.tokens;
+    r.row = job.s.first + 2 * job.j * p.per;
     r.rows[0] = tokens_of(p, 0) * p.a.G;
     r.rows[1] = tokens_of(p, 1) * p.a.G;
   }
   // Tokens of tile t, and the end of the units that it takes part in.
   MK_DEV int tokens_of(const PfArgs& p, int t) const {
-    const int per = p.tokens / 2;
-    return min(per, job.s.n - job.j * p.tokens - t * per);
+    return min(p.per, job.s.n - (2 * job.j + t) * p.per);
   }
   MK_DEV int end_of(const PfArgs& p, int t) const {
     const int n = tokens_of(p, t);
     if (n <= 0) return ka;
-    const int last = job.j * p.tokens + t * (p.tokens / 2) + n - 1;
+    const int last = (2 * job.j + t) * p.per + n - 1;
     return max(ka, min(kb, (pf_seen(job.s, last) + PF_UNIT - 1) / PF_UNIT));
   }
 };
@@ -624,7 +623,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
           continue;
         }
         if (is_v) {  // the queries: one box of whole tokens and their heads per tile
-          const int tile_rows = p.tokens / 2 * a.G;
+          const int tile_rows = p.per * a.G;
 #pragma unroll
           for (int t = 0; t < 2; t++) {
             if (w.e[t] == w.ka) continue;
@@ -638,7 +637,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
               mbar_expect_tx(bar, (uint32_t)tile_rows * D * 2);
 #pragma unroll
               for (int c = 0; c < C; c++)
-                tma_load_3d(dst + c * 16384, &qmap, 64 * c, w.h * a.G, w.row + t * (p.tokens / 2), bar,
+                tma_load_3d(dst + c * 16384, &qmap, 64 * c, w.h * a.G, w.row + t * p.per, bar,
                             policy);
             }
             __syncwarp();
@@ -863,7 +862,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
     const uint32_t s_addr = tmem + lane_base + Sh::S_COL + 128 * t;
     const uint32_t o_addr = tmem + lane_base + Sh::O_COL + D * t;
     const uint32_t p_addr = SEP ? tmem + lane_base + Sh::P_COL + 64 * t : s_addr;
-    const int row = 128 * t + r, row_token = t * (p.tokens / 2) + r / a.G, row_head = r % a.G;
+    const int row = 128 * t + r, row_token = t * p.per + r / a.G, row_head = r % a.G;
     uint32_t taken = 0, sp = 0, vp = 0;  // records; phases of s_full and pv_done
     bool ok = true;
     PfRec w;
@@ -979,10 +978,13 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
         for (int c = 0; c < D; c += N) {
           uint32_t y[N];
           tmem_ldn<N>(o_addr + c, y);
-          float b[4] = {0.f, 0.f, 0.f, 0.f};
+          // (a sum is finite where all are, but for sums beyond the range: then the row is
+          // redone for nothing)
+          float2 b[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int i = 0; i < N; i++) b[i & 3] = fmaf(__uint_as_float(y[i]), 0.f, b[i & 3]);
-          bad += (b[0] + b[1]) + (b[2] + b[3]);
+          for (int i = 0; i < N; i += 2)
+            b[i >> 1 & 1] = fadd2(b[i >> 1 & 1], make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])));
+          bad += ((b[0].x + b[1].x) + (b[0].y + b[1].y)) * 0.f;
           if (mine && w.whole) {
             const float2 f = make_float2(inv, inv), zero = make_float2(0.f, 0.f);
 #pragma unroll
@@ -1125,7 +1127,7 @@ __global__ void __launch_bounds__(256) kv_prefill_join_kernel(const __grid_const
   }
   if (!live) return;
   const int hq = job.h * a.G + r % a.G;
-  const long long tok = job.row + tile * (p.tokens / 2) + r / a.G;
+  const long long tok = job.row + tile * p.per + r / a.G;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint16_t* out = (uint16_t*)a.o.p + tok * a.o.ts + hq * a.o.hs + warp * N * 4;
 #pragma unroll

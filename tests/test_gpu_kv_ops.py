@@ -604,3 +604,28 @@ def test_attention_workspace_is_checked():
         f(view, bt, 4, rows, 0.125, to, None, ws.data_ptr(), need)
         ref, _, A, err = c.reference(0.125)
         assert ((out.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -7 * A).all()
+
+
+@pytest.mark.parametrize("heads", [(2, 2, 64), (9, 3, 128), (64, 1, 64), (128, 1, 128), (30, 2, 64)])
+def test_prefill_head_groups(heads):
+    # group sizes that fill a tile of 128 rows exactly, nearly, and with one token
+    c = Case(heads, [190, 5, 400], [190, 5, 33], block=32, seed=31)
+    c.check("prefill", c.run("prefill"))
+
+
+def test_prefill_refuses_wide_groups():
+    c = Case((129, 1, 64), [5], [5], block=16, seed=32)
+    with pytest.raises(MkError):
+        c.run("prefill")
+
+
+@pytest.mark.parametrize("lens,new", [
+    ([5000] * 3, [5000, 1, 77]),           # jobs cut into many parts
+    ([1300] * 40, [40] * 40),              # many short chunks over long caches
+    ([20000, 3, 3, 3], [9, 3, 2, 1]),      # one sequence holds all the work
+    ([129] * 64, [129] * 64),              # more jobs than SMs, each two units
+])
+@pytest.mark.parametrize("heads", [(8, 2, 64), (4, 2, 128)])
+def test_prefill_cuts(heads, lens, new):
+    c = Case(heads, lens, new, block=64, seed=33)
+    c.check("prefill", c.run("prefill"))
