@@ -39,7 +39,4 @@ MK_DEV int part_of(long long total, int parts, long long u) {
   return (int)(((u + 1) * parts - 1) / total);
 }
 
-MK_DEV void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
-MK_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 }  // namespace mk

@@ -6,6 +6,12 @@
 
 namespace mk {
 
+// Programmatic dependent launch: every kernel here may be launched while the one
+// before it in the stream still runs, and waits for all of that one's work before it
+// reads or writes anything.
+MK_DEV void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
+MK_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // What the operators found since mk_kv_status() last looked (MK_OK or an
 // MK_ERR_* code; the first finding stays).
 __device__ int kv_status_word = 0;

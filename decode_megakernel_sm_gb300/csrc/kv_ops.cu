@@ -21,25 +21,15 @@ static int sm_count() {
   return n;
 }
 
-// Four tokens to a block keep more loads in flight for one look-up (25 us against 33
-// with one, 9833 tokens of 48 heads of 64); one token to a block starts sooner (3.2 us
-// against 4.1 for a single token), so few tokens take that.
-template <int D, bool F32>
-static void append_launch(const AppendArgs& a, int n_sm, cudaStream_t s) {
-  constexpr int NT = KV_APPEND_TOKENS;
-  const int n = a.bt.n_tokens;
-  if (n <= NT * n_sm) kv_append_kernel<D, F32, 1><<<n, KV_APPEND_THREADS, 0, s>>>(a);
-  else kv_append_kernel<D, F32, NT><<<(n + NT - 1) / NT, KV_APPEND_THREADS, 0, s>>>(a);
-}
-
 // Launch `kernel` so that it may start while the one before it in the stream
 // runs; it waits for that one itself (griddepcontrol.wait).
 template <typename... P>
-static cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned block,
-                                    cudaStream_t s, P... args) {
+static cudaError_t launch(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem,
+                          cudaStream_t s, const P&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -47,6 +37,17 @@ static cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned bl
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Four tokens to a block keep more loads in flight for one look-up (25 us against 33
+// with one, 9833 tokens of 48 heads of 64); one token to a block starts sooner (3.2 us
+// against 4.1 for a single token), so few tokens take that.
+template <int D, bool F32>
+static void append_launch(const AppendArgs& a, int n_sm, cudaStream_t s) {
+  constexpr int NT = KV_APPEND_TOKENS;
+  const int n = a.bt.n_tokens;
+  if (n <= NT * n_sm) launch(kv_append_kernel<D, F32, 1>, dim3(n), KV_APPEND_THREADS, 0, s, a);
+  else launch(kv_append_kernel<D, F32, NT>, dim3((n + NT - 1) / NT), KV_APPEND_THREADS, 0, s, a);
 }
 
 // Query heads of one item of the decode kernel: 8 fill half of a tensor-core
@@ -65,9 +66,9 @@ static int decode_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
   const int grid = n_sm * Sh::BLOCKS;
   const long long rows = (long long)a.bt.batch * a.Hq;
   if (rows > 0x7FFFFFFFll) return MK_ERR_UNSUPPORTED;
-  kv_decode_kernel<D, NT><<<grid, DEC_THREADS, 0, s>>>(a);
-  if (launch_dependent(kv_decode_join_kernel<D, NT>, dim3((unsigned)rows), 32 * JOIN_WARPS, s, a, grid) !=
-      cudaSuccess)
+  if (launch(kv_decode_kernel<D, NT>, dim3(grid), DEC_THREADS, 0, s, a) != cudaSuccess ||
+      launch(kv_decode_join_kernel<D, NT>, dim3((unsigned)rows), 32 * JOIN_WARPS, 0, s, a, grid) !=
+          cudaSuccess)
     return MK_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
@@ -134,9 +135,10 @@ static int prefill_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return MK_ERR_CUDA;
-  kv_prefill_kernel<D><<<n_sm, PF_THREADS, PfShape<D>::SMEM, s>>>(p, maps[0], maps[1], maps[2]);
-  if (n_sm > 1 && launch_dependent(kv_prefill_join_kernel<D>, dim3(n_sm - 1, PF_ROWS / 32), 256, s,
-                                   p, n_sm) != cudaSuccess)
+  if (launch(kv_prefill_kernel<D>, dim3(n_sm), PF_THREADS, PfShape<D>::SMEM, s, p, maps[0],
+             maps[1], maps[2]) != cudaSuccess ||
+      (n_sm > 1 && launch(kv_prefill_join_kernel<D>, dim3(n_sm - 1, PF_ROWS / 32), 256, 0, s, p,
+                          n_sm) != cudaSuccess))
     return MK_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }

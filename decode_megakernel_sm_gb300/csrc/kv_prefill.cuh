@@ -572,6 +572,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), 512);
+  pdl_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
