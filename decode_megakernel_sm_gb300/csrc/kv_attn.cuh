@@ -33,10 +33,4 @@ MK_DEV float state_lse(float m, float l) { return l == 0.f ? -INFINITY : (m + lo
 // Split of `total` units of work over `parts` blocks: block i's first unit.
 MK_DEV long long part_begin(long long total, int parts, int i) { return total * i / parts; }
 
-// The block whose range holds unit u (total > 0, parts <= total): the largest
-// i with part_begin(i) <= u.
-MK_DEV int part_of(long long total, int parts, long long u) {
-  return (int)(((u + 1) * parts - 1) / total);
-}
-
 }  // namespace mk

@@ -55,13 +55,6 @@ MK_DEV long long dec_total(const KvView& kv, const KvBatch& bt, int lane) {
   return n;
 }
 
-// Units before sequence b, one item per sequence (one warp, all lanes).
-MK_DEV long long dec_before(const KvView& kv, const KvBatch& bt, int b, int lane) {
-  KvBatch first = bt;
-  first.batch = b;
-  return dec_total(kv, first, lane);
-}
-
 // The place of unit u of the line (one warp, all lanes).
 MK_DEV DecPlace dec_find(const KvView& kv, const KvBatch& bt, int items, long long u, int lane) {
   long long before = 0;
@@ -392,13 +385,52 @@ kv_decode_kernel(const __grid_constant__ AttnArgs a) {
   }
 }
 
-// One block per (sequence, query head): joins the states of the blocks that
-// shared its item.  What it needs besides the states is found before it waits
-// for the first kernel; then every warp takes every JOIN_WARPS-th state, all
-// loads of four states in flight at once.
+// How the line of units is cut, for the join: block i of `parts` begins at begin(i),
+// which is part_begin() in 32 bits (the launch refuses more units).
+struct DecLine {
+  unsigned total, quot, rest;
+  int parts;
+  MK_DEV unsigned begin(int i) const { return quot * i + rest * (unsigned)i / (unsigned)parts; }
+  // The block whose range holds unit u < total.
+  MK_DEV int part_of(unsigned u) const {
+    int i = min((int)((float)u / (float)total * parts), parts - 1);
+    while (i > 0 && begin(i) > u) i--;
+    while (i + 1 < parts && begin(i + 1) <= u) i++;
+    return i;
+  }
+};
+
+// The line of the whole batch, and the units before sequence b (one warp, all
+// lanes; len0: rows of this lane's sequence among the first 32).
+MK_DEV DecLine dec_line(const KvView& kv, const KvBatch& bt, int items, int grid, int len0, int b,
+                        unsigned& before, int lane) {
+  unsigned n = 0, m = 0;
+  for (int i = lane; i < bt.batch; i += 32) {
+    const unsigned u = dec_units(i < 32 ? len0 : kv_len(kv, bt, i));
+    n += u;
+    if (i < b) m += u;
+  }
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) {
+    n += __shfl_xor_sync(0xFFFFFFFFu, n, w);
+    m += __shfl_xor_sync(0xFFFFFFFFu, m, w);
+  }
+  before = m * items;
+  DecLine l;
+  l.total = n * items;
+  l.parts = (int)min((unsigned)grid, l.total);
+  l.quot = l.total / l.parts;
+  l.rest = l.total - l.quot * l.parts;
+  return l;
+}
+
+// Joins the states of the blocks that shared a row's item, W warps to a (sequence,
+// query head): each takes every W-th state, four at a time with all their loads in
+// flight.  What a warp needs besides the states it finds before it waits for the
+// first kernel.
 constexpr int JOIN_WARPS = 8;
 
-template <int D, int NT>
+template <int D, int NT, int W>
 __global__ void __launch_bounds__(32 * JOIN_WARPS)
 kv_decode_join_kernel(const __grid_constant__ AttnArgs a, int grid) {
   using Sh = DecShape<D, NT>;
@@ -406,25 +438,28 @@ kv_decode_join_kernel(const __grid_constant__ AttnArgs a, int grid) {
   __shared__ float so[JOIN_WARPS][D], sm[JOIN_WARPS], sl[JOIN_WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int blocks_of_heads = (a.G + HB - 1) / HB, items = a.kv.Hkv * blocks_of_heads;
-  const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
-  const int hb = hq % a.G / HB, head = hq % a.G % HB;
+  const int row = blockIdx.x * (JOIN_WARPS / W) + warp / W, me = warp % W;
+  const bool live = row < a.bt.batch * a.Hq;
+  const int b = live ? row / a.Hq : 0, hq = row - b * a.Hq;
+  const int g = hq % a.G, hb = g / HB, head = g - hb * HB;
   const int item = hq / a.G * blocks_of_heads + hb;
   const int units = dec_units(kv_len(a.kv, a.bt, b));
-  const long long total = dec_total(a.kv, a.bt, lane) * items;
-  const long long first = dec_before(a.kv, a.bt, b, lane) * items + (long long)item * units;
-  const int parts = (int)min((long long)grid, total);
-  const int i0 = part_of(total, parts, first), i1 = part_of(total, parts, first + units - 1);
-  const int slot0 = part_begin(total, parts, i0) == first ? 0 : 1;
+  const int len0 = lane < a.bt.batch ? kv_len(a.kv, a.bt, lane) : 0;
+  unsigned first;
+  const DecLine line = dec_line(a.kv, a.bt, items, grid, len0, b, first, lane);
+  first += item * units;
+  const int i0 = live ? line.part_of(first) : 0, i1 = live ? line.part_of(first + units - 1) : 0;
+  const int slot0 = line.begin(i0) == first ? 0 : 1;
   pdl_wait();
-  if (i0 == i1) return;  // that block wrote the result
+  const bool split = live && i0 != i1;  // (else one block wrote the result)
   float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; e++) o[e] = 0.f;
-  for (int i = i0 + warp; i <= i1; i += N * JOIN_WARPS) {
+  for (int i = split ? i0 + me : 1 << 30; i <= i1; i += N * W) {
     float mi[N], li[N], oi[N][E];
 #pragma unroll
     for (int n = 0; n < N; n++) {
-      const int j = i + n * JOIN_WARPS;
+      const int j = i + n * W;
       const bool in = j <= i1;
       const float* st = a.ws + ((size_t)j * 2 + (j == i0 ? slot0 : 0)) * Sh::STATE;
       mi[n] = in ? st[HB * D + head] : -INFINITY;
@@ -445,36 +480,41 @@ kv_decode_join_kernel(const __grid_constant__ AttnArgs a, int grid) {
     for (int e = 0; e < E; e++) o[e] *= f;
 #pragma unroll
     for (int n = 0; n < N; n++) {
-      const float g = join_weight(mi[n], top);
-      l = fmaf(li[n], g, l);
+      const float y = join_weight(mi[n], top);
+      l = fmaf(li[n], y, l);
 #pragma unroll
-      for (int e = 0; e < E; e++) o[e] = fmaf(oi[n][e], g, o[e]);
+      for (int e = 0; e < E; e++) o[e] = fmaf(oi[n][e], y, o[e]);
     }
     m = top;
   }
+  if (W > 1) {
 #pragma unroll
-  for (int e = 0; e < E; e++) so[warp][lane * E + e] = o[e];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+    for (int e = 0; e < E; e++) so[warp][lane * E + e] = o[e];
+    if (lane == 0) {
+      sm[warp] = m;
+      sl[warp] = l;
+    }
+    __syncthreads();
+    if (!split || me != 0) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < W; w++) top = fmaxf(top, sm[warp + w]);
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; e++) o[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; w++) {
+      const float f = join_weight(sm[warp + w], top);
+      l = fmaf(sl[warp + w], f, l);
+#pragma unroll
+      for (int e = 0; e < E; e++) o[e] = fmaf(so[warp + w][lane * E + e], f, o[e]);
+    }
+    m = top;
   }
-  __syncthreads();
-  const int dim = 2 * threadIdx.x;
-  if (dim >= D) return;
-  float top = -INFINITY;
-  l = 0.f;
-  float2 x = make_float2(0.f, 0.f);
+  if (!split) return;
 #pragma unroll
-  for (int w = 0; w < JOIN_WARPS; w++) top = fmaxf(top, sm[w]);
-#pragma unroll
-  for (int w = 0; w < JOIN_WARPS; w++) {
-    const float f = join_weight(sm[w], top);
-    l = fmaf(sl[w], f, l);
-    x.x = fmaf(so[w][dim], f, x.x);
-    x.y = fmaf(so[w][dim + 1], f, x.y);
-  }
-  attn_store2(a, b, hq, dim, x.x, x.y, l);
-  if (a.lse && dim == 0) a.lse[(long long)b * a.Hq + hq] = state_lse(top, l);
+  for (int e = 0; e < E; e += 2) attn_store2(a, b, hq, lane * E + e, o[e], o[e + 1], l);
+  if (a.lse && lane == 0) a.lse[(long long)b * a.Hq + hq] = state_lse(m, l);
 }
 
 }  // namespace mk
