@@ -10,6 +10,8 @@ import torch
 from . import _lib as L
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_empty = torch.empty
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 # The C structures as packed bytes, and the entry points that take them so.
 _VIEW = struct.Struct("=QQiiiiQi4x")  # mk_kv_view
@@ -20,9 +22,7 @@ _scratch = {}  # scratch bytes by device, operator and sizes
 
 
 def _call(name):
-    f = _entry.get(name)
-    if f is None:
-        f = _entry[name] = L.packed(name)
+    f = _entry[name] = L.packed(name)
     return f
 
 
@@ -67,12 +67,14 @@ class KVCache:
                                 tp, stride)
 
     # -- marshalling --------------------------------------------------------
-    def _rows(self, t, name, dtype, n=None, heads=None):
+    def _rows(self, t, name, dtype, n, heads):
         """mk_rows of t, which has to be [n][heads][dim] (None: any)."""
-        s = t.shape
-        if len(s) != 3 or t.dtype is not dtype or t.get_device() != self._index or \
-                s[2] != self.dim or (n is not None and s[0] != n) or \
-                (heads is not None and s[1] != heads):
+        try:
+            a, b, c = t.shape
+        except ValueError:
+            a = b = c = -1
+        if c != self.dim or t.dtype is not dtype or t.get_device() != self._index or \
+                (n is not None and a != n) or (heads is not None and b != heads):
             raise ValueError(f"{name}: expected {dtype} [{'tokens' if n is None else n}]"
                              f"[{'heads' if heads is None else heads}][{self.dim}] on {self.device}")
         ts, hs, one = t.stride()
@@ -81,7 +83,7 @@ class KVCache:
         if t.requires_grad and torch.is_grad_enabled():
             raise ValueError(f"{name}: the cache operators have no backward pass")
         # the stride of a dimension of one means nothing
-        return _ROWS.pack(t.data_ptr(), ts if s[0] > 1 else 0, hs if s[1] > 1 else 0)
+        return _ROWS.pack(t.data_ptr(), ts if a > 1 else 0, hs if b > 1 else 0)
 
     def _vector(self, t, name, n):
         if t.dtype is not _I32 or t.dim() != 1 or t.get_device() != self._index or \
@@ -104,11 +106,9 @@ class KVCache:
 
     def _on(self, stream, tensors, call, *args):
         """call(raw stream, *args) with the cache's device and `stream` current."""
-        if stream is None and torch.cuda.current_device() == self._index:
-            return call(torch._C._cuda_getCurrentRawStream(self._index), *args)
         with torch.cuda.device(self.device):
             if stream is None:
-                return call(torch.cuda.current_stream().cuda_stream, *args)
+                return call(_raw_stream(self._index), *args)
             if not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(getattr(stream, "value", stream) or 0)
             for t in tensors:  # their memory is not reused before the stream is done with it
@@ -119,7 +119,7 @@ class KVCache:
 
     def _dense(self, n, heads):
         """A new bf16 [n][heads][dim] tensor and its mk_rows."""
-        t = torch.empty((n, heads, self.dim), dtype=_BF16, device=self.device)
+        t = _empty((n, heads, self.dim), dtype=_BF16, device=self.device)
         return t, _ROWS.pack(t.data_ptr(), heads * self.dim, self.dim)
 
     # -- operators ----------------------------------------------------------
@@ -141,24 +141,29 @@ class KVCache:
         bt, _ = self._batch(lens, cu, n)
         hq, qr, given = 0, None, None
         if q is not None:
-            qr, hq = self._rows(q, "q", src, n), q.shape[1]
+            qr, hq = self._rows(q, "q", src, n, None), q.shape[1]
             if q_out is not None:
                 given = self._rows(q_out, "q_out", _BF16, n, hq)
+        src = 1 if src is _F32 else 0  # MK_SRC_F32, MK_SRC_BF16
+        if stream is None and _device() == self._index:
+            return self._append(_raw_stream(self._index), bt, n, hq, qr, kr, vr, src, q_out, given,
+                                theta)
         return self._on(stream, (q, k, v, lens, cu, q_out, self.k, self.v, self.table),
-                        self._append, bt, n, hq, qr, kr, vr, int(src is _F32), q_out, given, theta)
+                        self._append, bt, n, hq, qr, kr, vr, src, q_out, given, theta)
 
     def _append(self, raw, bt, n, hq, qr, kr, vr, src, out, rows, theta):
         if qr is None:
             out = None
         elif rows is None:
             out, rows = self._dense(n, hq)
-        status = _call("mk_kv_append")(self._view, bt, hq, qr, kr, vr, src, rows, theta, raw)
+        status = (_entry.get("mk_kv_append") or _call("mk_kv_append"))(
+            self._view, bt, hq, qr, kr, vr, src, rows, theta, raw)
         if status:
             raise L.MkError(status, "mk_kv_append")
         return out
 
     def _attend(self, decode, q, lens, cu, scale, out, return_lse, stream):
-        qr = self._rows(q, "q", _BF16)
+        qr = self._rows(q, "q", _BF16, None, None)
         n, hq, _ = q.shape
         bt, batch = self._batch(lens, cu, n)
         given = None if out is None else self._rows(out, "out", _BF16, n, hq)
@@ -170,18 +175,23 @@ class KVCache:
             if len(_scratch) >= 1024:
                 _scratch.clear()
             _scratch[key] = need
+        name = "mk_attn_decode" if decode else "mk_attn_prefill"
+        if scale is None:
+            scale = self.dim ** -0.5
+        if stream is None and _device() == self._index:
+            return self._launch(_raw_stream(self._index), name, bt, n, hq, qr, scale, out, given,
+                                return_lse, need)
         return self._on(stream, (q, lens, cu, out, self.k, self.v, self.table), self._launch,
-                        "mk_attn_decode" if decode else "mk_attn_prefill", bt, n, hq, qr,
-                        self.dim ** -0.5 if scale is None else scale, out, given, return_lse, need)
+                        name, bt, n, hq, qr, scale, out, given, return_lse, need)
 
     def _launch(self, raw, name, bt, n, hq, qr, scale, out, rows, return_lse, need):
         if rows is None:
             out, rows = self._dense(n, hq)
-        lse = torch.empty((n, hq), dtype=_F32, device=self.device) if return_lse else None
-        ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
-        status = _call(name)(self._view, bt, hq, qr, scale, rows,
-                             lse.data_ptr() if return_lse else None,
-                             ws.data_ptr() if need else None, need, raw)
+        ws = _empty(need, dtype=torch.uint8, device=self.device) if need else None
+        lse = _empty((n, hq), dtype=_F32, device=self.device) if return_lse else None
+        status = (_entry.get(name) or _call(name))(
+            self._view, bt, hq, qr, scale, rows, lse.data_ptr() if return_lse else None,
+            ws.data_ptr() if need else None, need, raw)
         if status:
             raise L.MkError(status, name)
         return (out, lse) if return_lse else out

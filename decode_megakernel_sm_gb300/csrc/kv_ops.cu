@@ -21,10 +21,10 @@ static int sm_count() {
   return n;
 }
 
-// Launch `kernel` so that it may start while the one before it in the stream
-// runs; it waits for that one itself (griddepcontrol.wait).
+// Launch a kernel; `early`: so that it may start while the one before it in the
+// stream still runs, which it waits for itself (griddepcontrol.wait).
 template <typename... P>
-static cudaError_t launch(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem,
+static cudaError_t launch(bool early, void (*kernel)(P...), dim3 grid, unsigned block, size_t smem,
                           cudaStream_t s, const P&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
@@ -35,7 +35,7 @@ static cudaError_t launch(void (*kernel)(P...), dim3 grid, unsigned block, size_
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -46,8 +46,8 @@ template <int D, bool F32>
 static void append_launch(const AppendArgs& a, int n_sm, cudaStream_t s) {
   constexpr int NT = KV_APPEND_TOKENS;
   const int n = a.bt.n_tokens;
-  if (n <= NT * n_sm) launch(kv_append_kernel<D, F32, 1>, dim3(n), KV_APPEND_THREADS, 0, s, a);
-  else launch(kv_append_kernel<D, F32, NT>, dim3((n + NT - 1) / NT), KV_APPEND_THREADS, 0, s, a);
+  if (n <= NT * n_sm) launch(false, kv_append_kernel<D, F32, 1>, dim3(n), KV_APPEND_THREADS, 0, s, a);
+  else launch(false, kv_append_kernel<D, F32, NT>, dim3((n + NT - 1) / NT), KV_APPEND_THREADS, 0, s, a);
 }
 
 // Query heads of one item of the decode kernel: 8 fill half of a tensor-core
@@ -63,7 +63,7 @@ static size_t decode_ws(int n_sm) {
 template <int D, int NT, int W>
 static cudaError_t join_launch(const AttnArgs& a, int grid, long long rows, cudaStream_t s) {
   constexpr int PER = JOIN_WARPS / W;
-  return launch(kv_decode_join_kernel<D, NT, W>, dim3((unsigned)((rows + PER - 1) / PER)),
+  return launch(true, kv_decode_join_kernel<D, NT, W>, dim3((unsigned)((rows + PER - 1) / PER)),
                 32 * JOIN_WARPS, 0, s, a, grid);
 }
 
@@ -74,7 +74,7 @@ static int decode_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
   const long long rows = (long long)a.bt.batch * a.Hq;
   const long long items = (long long)a.bt.batch * a.kv.Hkv * ((a.G + Sh::HB - 1) / Sh::HB);
   if (rows > 0x7FFFFFFFll || items > 0x7FFFFFFFll / (a.kv.cap / DEC_UNIT + 1)) return MK_ERR_UNSUPPORTED;
-  if (launch(kv_decode_kernel<D, NT>, dim3(grid), DEC_THREADS, 0, s, a) != cudaSuccess)
+  if (launch(false, kv_decode_kernel<D, NT>, dim3(grid), DEC_THREADS, 0, s, a) != cudaSuccess)
     return MK_ERR_CUDA;
   // Warps per row of the join: where items are few, each is split into many states
   // (about grid / items): 8 items of 32768 rows 18.9 us with eight warps, 20.0 with
@@ -147,9 +147,9 @@ static int prefill_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return MK_ERR_CUDA;
-  if (launch(kv_prefill_kernel<D>, dim3(n_sm), PF_THREADS, PfShape<D>::SMEM, s, p, maps[0],
+  if (launch(false, kv_prefill_kernel<D>, dim3(n_sm), PF_THREADS, PfShape<D>::SMEM, s, p, maps[0],
              maps[1], maps[2]) != cudaSuccess ||
-      (n_sm > 1 && launch(kv_prefill_join_kernel<D>, dim3(n_sm - 1, PF_ROWS / 32), 256, 0, s, p,
+      (n_sm > 1 && launch(true, kv_prefill_join_kernel<D>, dim3(n_sm - 1, PF_ROWS / 32), 256, 0, s, p,
                           n_sm) != cudaSuccess))
     return MK_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
