@@ -798,28 +798,26 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
           if (j < e) qk(t, j + 1 == e);
           k_next();
         };
-        auto take = [&]() {  // the next job with anything to do
-          bool got;
-          do {
-            got = pf_take(sh, taken, w, lane == 0);
-          } while (got && w.ka == max(w.e[0], w.e[1]));
+        // The next job and its first S.  One job only, though it may have no units:
+        // the record behind it may have to wait for the products not yet issued.
+        auto take = [&]() {
+          const bool got = pf_take(sh, taken, w, lane == 0);
+          if (got && w.ka < max(w.e[0], w.e[1])) s_of(w.ka, w.ka, t == 0 ? w.e[0] : w.e[1]);
           return got;
         };
         bool more = take();
-        if (more) s_of(w.ka, w.ka, t == 0 ? w.e[0] : w.e[1]);
         while (more && ok) {
           const int ka = w.ka, e = t == 0 ? w.e[0] : w.e[1], kb = max(w.e[0], w.e[1]);
           for (int j = ka; j < kb && ok; j++) {
-            if (j + 1 < kb) {
+            if (j + 1 < kb)
               s_of(j + 1, ka, e);
-            } else {
+            else
               more = take();
-              if (more) s_of(w.ka, w.ka, t == 0 ? w.e[0] : w.e[1]);
-            }
             wait(&sh.v_full[vs], vp);
             if (j < e) pv(t, j == ka, j + 1 == e);
             v_next();
           }
+          if (ka == kb) more = take();
         }
       } else if (warp == 1) {
         // 128-dim heads, one warp: the products bound them, and the tiles take turns

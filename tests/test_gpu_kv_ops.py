@@ -629,3 +629,12 @@ def test_prefill_refuses_wide_groups():
 def test_prefill_cuts(heads, lens, new):
     c = Case(heads, lens, new, block=64, seed=33)
     c.check("prefill", c.run("prefill"))
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 64), (4, 2, 128)])
+def test_prefill_runs_of_jobs_without_rows(heads):
+    """Most sequences of a padded batch hold no rows at all: a block's piece of the
+    work then has runs of jobs with nothing to multiply between the others."""
+    lens = [(40 + 7 * b if b % 10 == 3 else 0) for b in range(600)]
+    c = Case(heads, lens, [33] * 600, block=16, seed=51)
+    c.check("prefill", c.run("prefill"))
