@@ -36,13 +36,14 @@ class KVCache:
     rows, the new tokens' included, and ``cu`` (int32 [batch + 1]) the offsets of
     the sequences' new tokens in the rows of q, k, v and the outputs; cu None:
     one new token per sequence.  The new tokens are the last ones of their
-    sequences.  Rows from cu[batch] on are padding, neither read nor written.
+    sequences.  Rows before cu[0] and from cu[batch] on are padding: not written,
+    and what they hold has no effect.
 
     Calls run asynchronously on ``stream`` (default: the current one), allocate
     their scratch, and their outputs unless given, from torch's allocator, and
     may be captured into a CUDA graph.  Outputs carry no gradients.  What the
-    kernels find in lens, cu and table (a length the cache cannot hold, a block
-    outside the pool) is kept for ``check``."""
+    kernels find in lens, cu and table (a length the cache cannot hold, offsets
+    that fall, a block outside the pool) is kept for ``check``."""
 
     __slots__ = ("k", "v", "table", "device", "heads", "dim", "held", "_index", "_view")
 

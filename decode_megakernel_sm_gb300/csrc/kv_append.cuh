@@ -82,8 +82,10 @@ __global__ void __launch_bounds__(KV_APPEND_THREADS) kv_append_kernel(const __gr
       int p = -1;
       long long r = -1;
       if (b < a.bt.batch) {
-        const int after = a.bt.cu ? __ldg(a.bt.cu + b + 1) - t : 1;
-        p = kv_len(a.kv, a.bt, b) - after;
+        int first, n;
+        kv_new_tokens(a.bt, b, first, n);
+        // (a row before the first sequence, or offsets that fall: no token of b)
+        if (first <= t && t < first + n) p = kv_len(a.kv, a.bt, b) - (first + n - t);
         if (p >= 0) r = kv_row_of(a.kv, b, 0, p);
       }
       pos[warp] = p;

@@ -77,15 +77,18 @@ MK_DEV long long kv_row_of(const KvView& kv, int b, int h, int p) {
   return ((long long)blk * kv.Hkv + h) * kv.block + r;
 }
 
-// First row of sequence b's new tokens in q / k / v / out, and their number.
+// First row of sequence b's new tokens in q / k / v / out, and their number;
+// offsets that fall or leave the rows are cut to them and reported.
 MK_DEV void kv_new_tokens(const KvBatch& bt, int b, int& first, int& n) {
   if (!bt.cu) {
     first = b;
     n = 1;
     return;
   }
-  first = min(max(__ldg(bt.cu + b), 0), bt.n_tokens);
-  n = max(min(__ldg(bt.cu + b + 1), bt.n_tokens) - first, 0);
+  const int from = __ldg(bt.cu + b), to = __ldg(bt.cu + b + 1);
+  if (from < 0 || to < from || to > bt.n_tokens) kv_fail(MK_ERR_INVALID_ARG);
+  first = min(max(from, 0), bt.n_tokens);
+  n = max(min(to, bt.n_tokens) - first, 0);
 }
 
 // Sequence that new token t belongs to (batch: none, a padding row), found by

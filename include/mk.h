@@ -201,9 +201,9 @@ int mk_set_kv_pages(mk_handle* h, int block, int n_blocks, const int32_t* d_tabl
  * mk_kv_batch: what is in the batch.  d_lens[b]: rows of sequence b's cache,
  *   the new tokens' included.  d_cu: [batch + 1] offsets, sequence b's new
  *   tokens are rows [d_cu[b], d_cu[b + 1]) of q, k, v and the outputs
- *   (d_cu[0] = 0, non-decreasing, d_cu[batch] <= n_tokens; rows from
- *   d_cu[batch] on are padding, neither read nor written); NULL: one new
- *   token per sequence, row b (n_tokens == batch).  The last new token of
+ *   (non-decreasing in [0, n_tokens]; rows before d_cu[0] and from
+ *   d_cu[batch] on are padding: not written, what they hold has no effect);
+ *   NULL: one new token per sequence, row b (n_tokens == batch).  The last new token of
  *   sequence b sits at position d_lens[b] - 1, the ones before it just below;
  *   a token whose position would be negative is not appended, and attends to
  *   nothing.
@@ -213,9 +213,10 @@ int mk_set_kv_pages(mk_handle* h, int block, int n_blocks, const int32_t* d_tabl
  * Errors, all three: MK_ERR_INVALID_ARG (NULL or misaligned pointers, sizes
  * or strides outside the above), MK_ERR_UNSUPPORTED, MK_ERR_CUDA.  Contents
  * of d_lens, d_cu and d_table are checked on the device: a length below 0 or
- * above what the view holds, or a block id outside [0, n_blocks) in a place
- * that is used, touches nothing outside the buffers, leaves that sequence's
- * outputs unspecified, and makes mk_kv_status() return MK_ERR_INVALID_ARG. */
+ * above what the view holds, offsets that fall or leave [0, n_tokens], or a
+ * block id outside [0, n_blocks) in a place that is used, touch nothing
+ * outside the buffers, leave the sequence's rows and outputs unspecified (bad
+ * offsets: the batch's), and make mk_kv_status() return MK_ERR_INVALID_ARG. */
 typedef struct {
   void* k;
   void* v;

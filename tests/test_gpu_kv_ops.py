@@ -638,3 +638,45 @@ def test_prefill_runs_of_jobs_without_rows(heads):
     lens = [(40 + 7 * b if b % 10 == 3 else 0) for b in range(600)]
     c = Case(heads, lens, [33] * 600, block=16, seed=51)
     c.check("prefill", c.run("prefill"))
+
+
+@pytest.mark.parametrize("kind", ["append", "prefill"])
+@pytest.mark.parametrize("cu", [[0, 9, 4, 12], [0, 4, 9, 13], [0, 4, 2 ** 31 - 1, 12], [0, -2 ** 31, 7, 12],
+                                [-3, 4, 9, 12]], ids=str)
+def test_offsets_that_fall_or_leave_the_rows(kind, cu):
+    """Bad offsets touch nothing outside the sequences' rows, and are reported."""
+    c = Case((4, 2, 64), [40, 21, 33], [4, 5, 3], block=16, seed=52)
+    bad = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    before = c.k.clone()
+    if kind == "append":
+        kv = torch.randn(c.n, 2, 64, device="cuda").to(BF)
+        c.cache.append(c.q, kv, kv, c.lens, bad, theta=1e4)
+        own = torch.zeros(c.k.shape[0], c.k.shape[2], dtype=torch.bool, device="cuda")
+        for b, n in enumerate(c.lens_l):
+            own[c.at(b, 0, n)] = True
+        same = (c.k.view(torch.int16) == before.view(torch.int16)).all(-1).all(1)
+        assert same[~own].all()
+    else:
+        c.cache.prefill(c.q, c.lens, bad)
+    with pytest.raises(MkError) as e:
+        c.cache.check()
+    assert e.value.status == MK_ERR_INVALID_ARG
+
+
+def test_rows_before_the_first_sequence_are_padding():
+    c = Case((4, 2, 64), [40, 21], [7, 5], block=16, seed=53)
+    want = c.run("prefill")[0]
+    q = torch.cat([torch.full_like(c.q[:3], math.nan), c.q])
+    cu = c.cu + 3
+    out = torch.full((c.n + 3, 4, 64), 3.0, dtype=BF, device="cuda")
+    c.cache.prefill(q, c.lens, cu, out=out)
+    assert torch.equal(out[3:], want) and (out[:3] == 3).all()
+    kv = torch.randn(c.n + 3, 2, 64, device="cuda").to(BF)
+    other = Case((4, 2, 64), [40, 21], [7, 5], block=16, seed=53)
+    out.fill_(3.0)
+    got = c.cache.append(q, kv, kv, c.lens, cu, theta=1e4, q_out=out)
+    ref = other.cache.append(c.q, kv[3:], kv[3:], other.lens, other.cu, theta=1e4)
+    assert torch.equal(got[3:], ref) and (got[:3] == 3).all()
+    for a, b in ((c.k, other.k), (c.v, other.v)):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    c.cache.check()
