@@ -54,6 +54,8 @@ class KVCache:
             raise ValueError("k, v: expected two 4-dimensional bf16 CUDA tensors of one shape")
         if not (k.is_contiguous() and v.is_contiguous()):
             raise ValueError("k, v: expected contiguous tensors")
+        if k.requires_grad or v.requires_grad:
+            raise ValueError("k, v: the cache operators have no backward pass")
         n_blocks, self.heads, block, self.dim = shape
         if table is None:
             self.held, tp, stride = n_blocks, 0, 0
@@ -112,6 +114,8 @@ class KVCache:
                 return call(_raw_stream(self._index), *args)
             if not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(getattr(stream, "value", stream) or 0)
+            if stream.device != self.device:
+                raise ValueError(f"stream: expected one of {self.device}")
             for t in tensors:  # their memory is not reused before the stream is done with it
                 if t is not None:
                     t.record_stream(stream)

@@ -73,7 +73,6 @@ __global__ void __launch_bounds__(KV_APPEND_THREADS) kv_append_kernel(const __gr
   __shared__ int pos[NT];          // -1: nothing to do
   __shared__ long long row0[NT];   // pool row of kv head 0, or -1 (no page)
   const int t0 = blockIdx.x * NT, nt = min(NT, a.bt.n_tokens - t0);
-  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp < nt) {
     const int t = t0 + warp;

@@ -6,9 +6,10 @@
 
 namespace mk {
 
-// Programmatic dependent launch: every kernel here may be launched while the one
-// before it in the stream still runs, and waits for all of that one's work before it
-// reads or writes anything.
+// Programmatic dependent launch: the kernels that join partial states start while the
+// one that makes them still runs, and wait for all of its work before they read any.
+// The others start plainly: on an idle stream, where a caller's every launch finds it,
+// the early start costs 3 to 10 us more than it saves.
 MK_DEV void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
 MK_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

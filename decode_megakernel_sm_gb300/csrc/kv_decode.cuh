@@ -238,7 +238,6 @@ kv_decode_kernel(const __grid_constant__ AttnArgs a) {
   __shared__ __align__(16) float so[DEC_WARPS][HB][LD];
   __shared__ float sm[DEC_WARPS][HB], sl[DEC_WARPS][HB];
   __shared__ unsigned redo;
-  pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int blocks_of_heads = (a.G + HB - 1) / HB, items = a.kv.Hkv * blocks_of_heads;

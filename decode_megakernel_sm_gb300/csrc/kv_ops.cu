@@ -1,7 +1,10 @@
 // kv_ops.cu -- the KV-cache operators' entry points: checks of the arguments,
 // choice of the kernel, launch.  No state, no allocation.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <cstdlib>
+#include <limits>
 
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -107,14 +110,14 @@ static bool prefill_ready() {
   static std::atomic<uint64_t> known{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  const uint64_t bit = 1ull << (dev & 63);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (known.load(std::memory_order_relaxed) & bit) return true;
   cudaFuncAttributes at{};
   if (cudaFuncGetAttributes(&at, kv_prefill_kernel<D>) != cudaSuccess || at.numRegs != PF_REGS ||
       cudaFuncSetAttribute(kv_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            PfShape<D>::SMEM) != cudaSuccess)
     return false;
-  if (dev < 64) known.fetch_or(bit, std::memory_order_relaxed);
+  known.fetch_or(bit, std::memory_order_relaxed);
   return true;
 }
 
@@ -128,8 +131,9 @@ static int prefill_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
   p.a = a;
   p.per = PF_ROWS / 2 / a.G;
   p.negate = a.scale < 0.f;
-  // (a scale of zero: so small that every finite score rounds to the same weight)
-  p.scale2 = std::fmax(std::fabs(a.scale) * LOG2E, 1e-30f);
+  // (a scale of zero: the smallest number, which keeps masked scores at -inf and takes
+  // finite ones to below 2^-20)
+  p.scale2 = std::fmax(std::fabs(a.scale) * LOG2E, std::numeric_limits<float>::denorm_min());
   p.box = a.kv.table && a.kv.block < PF_UNIT ? a.kv.block : PF_UNIT;
   CUtensorMap maps[3];
   const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)D * 2};
@@ -164,6 +168,14 @@ static bool rows_ok(const mk_rows* r, size_t size) {
          (r->head_stride * (long)size) % 16 == 0;
 }
 
+// Rows that are written: no two of the [n][heads] overlap (the strides nest).
+static bool out_ok(const mk_rows* r, int n, int heads, int D) {
+  if (!rows_ok(r, 2)) return false;
+  const long long ts = std::llabs(r->token_stride), hs = std::llabs(r->head_stride);
+  if (n == 1 || heads == 1) return (n == 1 || ts >= D) && (heads == 1 || hs >= D);
+  return ts > hs ? hs >= D && ts >= hs * (heads - 1) + D : ts >= D && hs >= ts * (n - 1) + D;
+}
+
 static Rows rows(const mk_rows* r) { return Rows{r->p, r->token_stride, r->head_stride}; }
 
 // Fills the device structs; MK_OK, or why not.
@@ -186,7 +198,8 @@ static int check(const mk_kv_view* kv, const mk_kv_batch* bt, KvView& v, KvBatch
   if (kv->head_dim != 64 && kv->head_dim != 128) return MK_ERR_UNSUPPORTED;
   v = KvView{(const uint16_t*)kv->k, (const uint16_t*)kv->v, kv->d_table, kv->table_stride,
              kv->n_blocks, kv->n_kv_heads, kv->block, shift,
-             kv->d_table ? (long long)kv->table_stride * kv->block : kv->block};
+             std::min(kv->d_table ? (long long)kv->table_stride * kv->block : (long long)kv->block,
+                      0x7FFFF000ll)};  // (a length may be rounded up to units)
   b = KvBatch{bt->d_lens, bt->d_cu, bt->batch, bt->n_tokens};
   return MK_OK;
 }
@@ -209,7 +222,7 @@ extern "C" int mk_kv_append(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q
     return MK_ERR_INVALID_ARG;
   if (bt->n_tokens == 0 || bt->batch == 0) return MK_OK;
   if (!rows_ok(k, size) || !rows_ok(v, size) ||
-      (n_q_heads > 0 && (!rows_ok(q, size) || !rows_ok(q_out, 2))))
+      (n_q_heads > 0 && (!rows_ok(q, size) || !out_ok(q_out, bt->n_tokens, n_q_heads, kv->head_dim))))
     return MK_ERR_INVALID_ARG;
   a.k = rows(k);
   a.v = rows(v);
@@ -274,8 +287,10 @@ static int attention(bool decode, const mk_kv_view* kv, const mk_kv_batch* bt, i
   if ((bt->d_cu != nullptr) == decode) return MK_ERR_INVALID_ARG;
   if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads) return MK_ERR_INVALID_ARG;
   if (bt->n_tokens == 0 || bt->batch == 0) return MK_OK;
-  if (!rows_ok(q, 2) || !rows_ok(out, 2) || (d_lse && !aligned(d_lse, 4)))
+  if (!std::isfinite(scale) || !rows_ok(q, 2) ||
+      !out_ok(out, bt->n_tokens, n_q_heads, kv->head_dim) || (d_lse && !aligned(d_lse, 4)))
     return MK_ERR_INVALID_ARG;
+  if (out->p == q->p) return MK_ERR_INVALID_ARG;  // q is read again after out is written
   size_t need = 0;
   const int wrc = mk_attn_workspace_bytes(decode, bt->n_tokens, bt->batch, n_q_heads,
                                           kv->n_kv_heads, kv->head_dim, &need);

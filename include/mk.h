@@ -208,7 +208,8 @@ int mk_set_kv_pages(mk_handle* h, int block, int n_blocks, const int32_t* d_tabl
  *   a token whose position would be negative is not appended, and attends to
  *   nothing.
  * mk_rows: rows [token][head][head_dim] at the given strides in elements; the
- *   last dimension is dense, every row starts on a 16-byte boundary.
+ *   last dimension is dense, every row starts on a 16-byte boundary.  Rows that
+ *   are written must not overlap (one of the two strides spans the other's rows).
  *
  * Errors, all three: MK_ERR_INVALID_ARG (NULL or misaligned pointers, sizes
  * or strides outside the above), MK_ERR_UNSUPPORTED, MK_ERR_CUDA.  Contents
@@ -262,7 +263,12 @@ int mk_kv_append(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q_heads, con
  * its output, whatever they hold.
  *   mk_attn_decode: one new token per sequence (bt->d_cu NULL): each reads
  *     all d_lens[b] rows.
- *   mk_attn_prefill: any number of new tokens per sequence, causal.
+ *   mk_attn_prefill: any number of new tokens per sequence, causal.  At most
+ *     128 query heads per kv head, and pools of less than 2^31 rows
+ *     (n_blocks * n_kv_heads * block).
+ * scale is finite; out is not q.  A call whose work cannot be numbered in 31
+ * bits (decode: batch * n_q_heads, or items of 64 rows when every sequence has
+ * all the rows that the view can hold) is MK_ERR_UNSUPPORTED.
  * d_ws: device scratch of at least mk_attn_workspace_bytes() bytes, 256-byte
  * aligned, for this call alone until it has run: calls that may overlap, and
  * graphs that may replay at the same time, need their own.  Its contents do

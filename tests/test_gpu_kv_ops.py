@@ -13,6 +13,9 @@ by at most 2^-8 of the value):
     product where the kernel makes one: WEIGHT below.
   lse: the score's error, plus 2^-20 (1 + |lse|) for exp, sum and log."""
 import math
+import pathlib
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -680,3 +683,86 @@ def test_rows_before_the_first_sequence_are_padding():
     for a, b in ((c.k, other.k), (c.v, other.v)):
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
     c.cache.check()
+
+
+def test_first_calls_may_be_captured():
+    """A process whose first use of the operators is inside a capture."""
+    code = """
+import torch
+from decode_megakernel_sm_gb300 import KVCache
+def case(d):
+    torch.manual_seed(d)
+    k = torch.zeros(2, 2, 300, d, dtype=torch.bfloat16, device="cuda")
+    new = [torch.randn(200, h, d, device="cuda").bfloat16() for h in (8, 2, 2)]
+    one = torch.randn(2, 8, d, device="cuda").bfloat16()
+    lens = torch.tensor([120, 80], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 120, 200], dtype=torch.int32, device="cuda")
+    cache = KVCache(k, k.clone())
+    def run():
+        q = cache.append(*new, lens, cu, theta=1e4)
+        return cache.prefill(q, lens, cu), cache.decode(one, lens)
+    return cache, run
+cases = [case(64), case(128)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = [run() for _, run in cases]
+graph.replay()
+torch.cuda.synchronize()
+for (cache, run), g in zip(cases, got):
+    for a, b in zip(run(), g):
+        assert a.abs().sum() > 0 and torch.equal(a, b)
+    cache.check()
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300,
+                   cwd=pathlib.Path(__file__).resolve().parents[1])
+
+
+def test_calls_at_once_on_two_streams():
+    cases = [Case((16, 4, 128), [900, 3000], [900, 200], block=64, seed=54),
+             Case((32, 8, 64), [2500, 400], [300, 400], block=16, seed=55)]
+    want = [c.run("prefill") for c in cases]
+    steps = [(c, torch.randn(2, c.hq, c.d, generator=c.g, device="cuda").to(BF)) for c in cases]
+    want_step = [c.cache.decode(q, c.lens) for c, q in steps]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for (c, q), w, ws, s in zip(steps, want, want_step, streams):
+            got.append((w, c.run("prefill", stream=s)))
+            got.append(((ws,), (c.cache.decode(q, c.lens, stream=s),)))
+    torch.cuda.synchronize()
+    for w, g in got:
+        assert all(torch.equal(a, b) for a, b in zip(w, g))
+    cases[0].cache.check()
+
+
+def test_prefill_redoes_rows_of_a_long_cache():
+    # a NaN among the last token's own values: all other rows of its tile are redone
+    c = Case((8, 2, 64), [100_000], [32], block=64, seed=56)
+    blk, row = c.at(0, 99_999, 100_000)
+    ro, rl, A, err = c.reference()
+    c.v[blk, 0, row, 5] = math.nan
+    out, _ = c.run("prefill")
+    tol = 2.0 ** -8 * ro.abs() + (2 * err + 2.0 ** -14 + WEIGHT["prefill"])[..., None] * A
+    ok = (out.double() - ro).abs() <= tol
+    assert ok[:31].all() and ok[31, 4:].all() and torch.isnan(out[31, :4, 5]).all()
+    assert ok[31, :4].sum() == 4 * 63
+    c.cache.check()
+
+
+def test_outputs_that_overlap_or_name_the_queries_are_refused():
+    c = Case((4, 2, 64), [40, 20], [1, 1], block=16, seed=57)
+    with pytest.raises(MkError):
+        c.cache.decode(c.q, c.lens, out=c.q)
+    with pytest.raises(MkError):
+        c.cache.decode(c.q, c.lens, out=torch.empty(1, 4, 64, dtype=BF, device="cuda").expand(2, 4, 64))
+    with pytest.raises(MkError):
+        c.cache.decode(c.q, c.lens, scale=math.nan)
+    with pytest.raises(ValueError, match="backward"):
+        KVCache(c.k.clone().requires_grad_(), c.v, c.table)
+    # queries may be spread out from fewer rows
+    one = c.q[:1].expand(2, 4, 64)
+    assert torch.equal(c.cache.decode(one, c.lens), c.cache.decode(one.contiguous(), c.lens))
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    assert torch.equal(c.cache.prefill(one, c.lens, cu), c.cache.prefill(one.contiguous(), c.lens, cu))

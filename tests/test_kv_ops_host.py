@@ -128,3 +128,23 @@ def test_cache_wants_cuda_tensors():
     t = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         KVCache(t, t)
+
+
+@pytest.mark.parametrize("ts,hs", [(0, 64), (256, 0), (192, 64), (64, 64), (64, 320), (256, 32)])
+def test_outputs_must_not_overlap(ts, hs):
+    # [7][4][64]: rows that share elements, at strides that inputs may have
+    bt = batch(n_tokens=7, d_cu=P)
+    assert append(bt=bt, qo=rows(ts=ts, hs=hs)) == L.MK_ERR_INVALID_ARG
+    assert attn("prefill", bt=bt, out=rows(2 * P, ts, hs)) == L.MK_ERR_INVALID_ARG
+
+
+def test_output_is_not_the_queries():
+    for kind in ("decode", "prefill"):
+        assert attn(kind, q=rows(P), out=rows(P)) == L.MK_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf")])
+def test_scales_are_finite(scale):
+    for kind, bt in (("decode", batch()), ("prefill", batch(n_tokens=7, d_cu=P))):
+        f = getattr(L.lib(), f"mk_attn_{kind}")
+        assert f(view(), bt, 4, rows(), scale, rows(2 * P), None, P, 1 << 40, None) == L.MK_ERR_INVALID_ARG
