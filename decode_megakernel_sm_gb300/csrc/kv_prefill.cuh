@@ -35,16 +35,17 @@
 // states that a dependent kernel joins.  Everything is found on the device
 // from lens and cu.
 //
-// The weights P are rounded to bf16 (2^-9 of each weight, the accuracy of the
-// output's own rounding); their sum is taken before the rounding.  Cache rows
+// The weights P are rounded to bf16 (2^-8 of each weight at most, as the output's
+// own rounding); their sum is taken before the rounding.  Cache rows
 // from len on are never part of a product: the tile that holds the end of a
 // sequence takes its values through cp.async with zeros behind the end.  Rows
 // that a query does not see have weight zero, which times an infinite or NaN
 // value of a later token would still be NaN: rows whose result is not finite
 // although their weights are, are redone by attn_row.
 //
-// Every wait is bounded in time; one that runs out sets the status word, and all
-// warps leave through the common end, which frees the tensor memory.
+// Every wait is bounded in time: where the block gets no further for two seconds, all
+// warps leave through the common end, which frees the tensor memory and sets the
+// status word.
 #pragma once
 #include <cuda.h>
 
@@ -371,26 +372,23 @@ struct PfShared {
   PfRec rec[PF_RECS];
   uint32_t tmem;
   volatile int abort;
+  // When waiting ends (globaltimer): put off by the key loader as it gets on, which
+  // hangs on all other roles, and by a warp that is about to redo a row.
+  unsigned long long limit;
 };
 
+MK_DEV void pf_put_off(PfShared& sh, unsigned long long ns) { atomicMax(&sh.limit, gtimer() + ns); }
+
 // Wait for phase `n` (counted from 0) of a barrier; false if the block gave up.
+// (Few instructions: some 30 places wait, and what they fetch counts.)
 MK_DEV bool pf_wait(PfShared& sh, const unsigned long long* bar, uint32_t n) {
   const uint32_t b = smem_u32(bar);
-  if (mbar_try(b, n & 1)) return true;
-  unsigned long long t0 = 0;
-  for (uint32_t it = 1;; it++) {
-    if (mbar_try(b, n & 1)) return true;
-    if ((it & 63) == 0) {
-      if (sh.abort) return false;
-      const unsigned long long t = gtimer();
-      if (t0 == 0) t0 = t;
-      if (t - t0 > PF_TIMEOUT_NS) {
-        sh.abort = 1;
-        kv_fail(MK_ERR_TIMEOUT);
-        return false;
-      }
-    }
+  for (uint32_t it = 0; !mbar_try(b, n & 1); it++) {
+    if ((it & 63) != 63) continue;
+    if (sh.abort) return false;
+    if (gtimer() > *(volatile unsigned long long*)&sh.limit) sh.abort = 1;
   }
+  return true;
 }
 
 // The next record (one warp): false if the block gave up or there are no more jobs.
@@ -569,10 +567,10 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
     }
     mbar_init(smem_u32(&sh.drain), 2);
     sh.abort = 0;
+    sh.limit = gtimer() + PF_TIMEOUT_NS;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), 512);
-  pdl_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -698,6 +696,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
             __syncwarp();
           }
           if (!is_v && j == w.ka) walk.next(p);  // while the copy runs
+          if (!is_v && (n & 63) == 0 && lane == 0) pf_put_off(sh, PF_TIMEOUT_NS);
         }
       }
       if (sh.abort) {  // given up: wait for the copies in flight, again with a limit
@@ -849,8 +848,11 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
       // the products in flight still read shared and write tensor memory
       if (lead) tc_commit(smem_u32(&sh.drain));
       const unsigned long long t0 = gtimer();
-      while (!mbar_try(smem_u32(&sh.drain), 0) && gtimer() - t0 < PF_TIMEOUT_NS) {
-      }
+      while (!mbar_try(smem_u32(&sh.drain), 0))
+        if (gtimer() - t0 > PF_TIMEOUT_NS) {
+          sh.abort = 1;
+          break;
+        }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -1029,6 +1031,8 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
         const int end = __shfl_sync(0xFFFFFFFFu, last, src) + 1;
         const int hh = w.h * a.G + __shfl_sync(0xFFFFFFFFu, row_head, src);
         const long long row_tok = w.row + __shfl_sync(0xFFFFFFFFu, row_token, src);
+        // (some 65 ns a cache row)
+        if (lane == 0) pf_put_off(sh, PF_TIMEOUT_NS + 1000ull * (unsigned)w.len);
         float m1, l1, o1[D / 32];
         attn_row<D>(a.kv, w.b, w.h, (const uint16_t*)a.q.p + row_tok * a.q.ts + hh * a.q.hs,
                     a.scale, ka * PF_UNIT, min(end, kb * PF_UNIT), m1, l1, o1);
@@ -1051,6 +1055,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  if (threadIdx.x == 0 && sh.abort) kv_fail(MK_ERR_TIMEOUT);
 }
 
 // Block (x, y): if part x + 1 is the first to begin inside its job, joins rows
