@@ -7,6 +7,9 @@
 // form one line, every block takes an equal piece of it, and a second kernel
 // joins the states of items that more than one block has a part of.  Lengths
 // are read on the device, so one captured graph serves growing sequences.
+// Caches that can only hold little take a cluster of blocks per item instead, in
+// one launch.  32 sequences of 16384-32768 rows, 8 kv heads of 64 (1.56 GB): 241.6 us,
+// 6.48 TB/s; one of 1024 rows 5.0 us (clusters; 6.3 by the line).
 //
 // A block has four warps; a warp takes 16 rows of a unit straight from global
 // memory into registers in the tensor cores' fragment layout, the next unit's
@@ -382,6 +385,168 @@ kv_decode_kernel(const __grid_constant__ AttnArgs a) {
     p = p1;
     p1 = p2;
   }
+}
+
+// ---- few rows: a cluster per item ---------------------------------------------
+// Where even full sequences are a few units for each block of a cluster, a cluster
+// takes an item: each block an equal share of its units, no search of a line, and
+// the blocks' states joined through distributed shared memory, in the same launch.
+
+MK_DEV uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+MK_DEV uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// All threads of the cluster; what they wrote before is there after it.
+MK_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Block `rank`'s copy of a shared variable, two floats of it.
+MK_DEV uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+MK_DEV float2 ld_cluster2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(DEC_THREADS, DecShape<D, NT>::BLOCKS)
+kv_decode_cluster_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int HB = DecShape<D, NT>::HB, S = D / 16, LD = D + 4;
+  __shared__ __align__(16) float so[DEC_WARPS][HB][LD];
+  __shared__ float sm[DEC_WARPS][HB], sl[DEC_WARPS][HB];
+  __shared__ __align__(16) float po[HB][D];  // this block's state
+  __shared__ float2 pml[HB];
+  __shared__ unsigned redo;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const int rank = (int)cluster_rank(), size = (int)cluster_size();
+  const int blocks_of_heads = (a.G + HB - 1) / HB, items = a.kv.Hkv * blocks_of_heads;
+  const int work = blockIdx.x / size, b = work / items, item = work % items;
+  const int h = item / blocks_of_heads, hb = item % blocks_of_heads;
+  const int head0 = h * a.G + hb * HB, n_heads = min(HB, a.G - hb * HB);
+  const uint16_t* q0 = (const uint16_t*)a.q.p + b * a.q.ts + head0 * a.q.hs;
+  const int len = kv_len(a.kv, a.bt, b);
+  const long long units = (len + DEC_UNIT - 1) / DEC_UNIT;
+  const int u0 = (int)(units * rank / size), u1 = (int)(units * (rank + 1) / size);
+  const float scale2 = a.scale * LOG2E;
+  if (threadIdx.x == 0) redo = 0;
+
+  // This warp's rows of unit u: their block, then the rows; how many count.
+  auto block_of = [&](int u) {
+    const int j = u * DEC_UNIT + 16 * warp;
+    return u < u1 && j < len ? kv_block_of(a.kv, b, j) : -1;
+  };
+  auto load = [&](DecRows<D>& rows, int u, int blk) {
+    const int j = u * DEC_UNIT + 16 * warp, n = min(16, len - j);
+    const int in = a.kv.table ? (j & (a.kv.block - 1)) : j;
+    rows.load(a.kv, blk < 0 ? -1 : ((long long)blk * a.kv.Hkv + h) * a.kv.block + in, n, lane);
+    return blk < 0 ? 0 : n;
+  };
+  DecWarp<D, NT> w;
+  DecRows<D> rows, ahead;
+  int blk = block_of(u0);
+  int nv = load(rows, u0, blk), nv1 = 0;
+  blk = block_of(u0 + 1);
+  w.init(q0, a.q.hs, n_heads, lane);
+  for (int u = u0; u < u1; u++) {
+    if (u + 1 < u1) {
+      nv1 = load(ahead, u + 1, blk);
+      blk = block_of(u + 2);
+    }
+    w.step(rows, nv, scale2, lane);
+    rows = ahead;
+    nv = nv1;
+  }
+#pragma unroll
+  for (int n = 0; n < NT; n++) {
+    float l = w.l[n];
+    l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+    l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+    if (c == 0) {
+      sm[warp][8 * n + r] = w.m[n];
+      sl[warp][8 * n + r] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < S; i++) {
+      const int dim = dec_dim(i, r);
+      *(float2*)&so[warp][8 * n + 2 * c][dim] = make_float2(w.o[i][n][0], w.o[i][n][2]);
+      *(float2*)&so[warp][8 * n + 2 * c + 1][dim] = make_float2(w.o[i][n][1], w.o[i][n][3]);
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n_heads * (D / 2); i += DEC_THREADS) {
+    const int head = i / (D / 2), dim = 2 * (i % (D / 2));
+    float top = -INFINITY, l = 0.f;
+    float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int v = 0; v < DEC_WARPS; v++) top = fmaxf(top, sm[v][head]);
+#pragma unroll
+    for (int v = 0; v < DEC_WARPS; v++) {
+      const float f = join_weight(sm[v][head], top);
+      const float2 y = *(const float2*)&so[v][head][dim];
+      l = fmaf(sl[v][head], f, l);
+      o.x = fmaf(y.x, f, o.x);
+      o.y = fmaf(y.y, f, o.y);
+    }
+    if (!isfinite(o.x + o.y) && isfinite(l)) atomicOr(&redo, 1u << head);
+    *(float2*)&po[head][dim] = o;
+    if (dim == 0) pml[head] = make_float2(top, l);
+  }
+  __syncthreads();
+  if (const unsigned mask = redo) {
+    for (int head = warp; head < n_heads; head += DEC_WARPS) {
+      if (!(mask >> head & 1u)) continue;
+      float m, l, o[D / 32];
+      attn_row<D>(a.kv, b, h, q0 + head * a.q.hs, a.scale, u0 * DEC_UNIT, min(len, u1 * DEC_UNIT), m, l, o);
+#pragma unroll
+      for (int e = 0; e < D / 32; e++) po[head][lane * (D / 32) + e] = o[e];
+      if (lane == 0) pml[head] = make_float2(m * LOG2E, l);
+    }
+  }
+  cluster_sync();
+  // pairs of dimensions, dealt out over the cluster; the states eight at a time
+  for (int i = rank * DEC_THREADS + threadIdx.x; i < n_heads * (D / 2); i += size * DEC_THREADS) {
+    const int head = i / (D / 2), dim = 2 * (i % (D / 2));
+    float m = -INFINITY, l = 0.f;
+    float2 o = make_float2(0.f, 0.f);
+    for (int k0 = 0; k0 < size; k0 += 8) {
+      float2 ml[8], y[8];
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const bool in = k0 + k < size;
+        ml[k] = in ? ld_cluster2(cluster_addr(&pml[head], k0 + k)) : make_float2(-INFINITY, 0.f);
+        y[k] = in ? ld_cluster2(cluster_addr(&po[head][dim], k0 + k)) : make_float2(0.f, 0.f);
+      }
+      float top = m;
+#pragma unroll
+      for (int k = 0; k < 8; k++) top = fmaxf(top, ml[k].x);
+      const float f = join_weight(m, top);
+      m = top;
+      l *= f;
+      o.x *= f;
+      o.y *= f;
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const float g = join_weight(ml[k].x, top);
+        if (ml[k].y == 0.f) continue;  // no weight
+        l = fmaf(ml[k].y, g, l);
+        o.x = fmaf(y[k].x, g, o.x);
+        o.y = fmaf(y[k].y, g, o.y);
+      }
+    }
+    attn_store2(a, b, head0 + head, dim, o.x, o.y, l);
+    if (a.lse && dim == 0) a.lse[(long long)b * a.Hq + head0 + head] = state_lse(m, l);
+  }
+  cluster_sync();  // the others may still read this block's state
 }
 
 // How the line of units is cut, for the join: block i of `parts` begins at begin(i),

@@ -70,12 +70,45 @@ static cudaError_t join_launch(const AttnArgs& a, int grid, long long rows, cuda
                 32 * JOIN_WARPS, 0, s, a, grid);
 }
 
+// Blocks of the cluster that takes an item, or 0 where the line does: as many of 1, 2,
+// 4, 8 as the SMs hold for all items (16 do not fit everywhere: 16 items of 128-dim
+// heads took 10 us where 8 take 5), as long as the longest sequence that the cache can
+// hold is 4 units for each.  A cluster is one launch and no search, but balances
+// nothing.  Line and clusters, in us, 8 kv heads of 64: one sequence of 1024 rows 6.3
+// and 4.8, of 2048 6.9 and 6.2, of 4096 8.1 and 8.5; 16 of 1024 12.9 and 9.7, one of
+// 1024 among 15 of 64 6.8 and 7.0.  With 8 units 16 of 2048 would gain (19.1 and 15.1),
+// one of 2048 among 15 of 64 would lose as much (7.6 and 11.3).  A caller that waits
+// for each call saves 3 us more for the second launch.
+static int cluster_size(long long items, int grid, long long cap) {
+  int size = 1;
+  if (items > grid) return 0;
+  while (size < 8 && items * size * 2 <= grid) size *= 2;
+  return cap <= 4ll * DEC_UNIT * size ? size : 0;
+}
+
+template <int D, int NT>
+static cudaError_t cluster_launch(const AttnArgs& a, int items, int size, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(items * size);
+  cfg.blockDim = dim3(DEC_THREADS);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = size;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_decode_cluster_kernel<D, NT>, a);
+}
+
 template <int D, int NT>
 static int decode_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
   using Sh = DecShape<D, NT>;
   const int grid = n_sm * Sh::BLOCKS;
   const long long rows = (long long)a.bt.batch * a.Hq;
   const long long items = (long long)a.bt.batch * a.kv.Hkv * ((a.G + Sh::HB - 1) / Sh::HB);
+  if (const int size = cluster_size(items, grid, a.kv.cap))
+    return cluster_launch<D, NT>(a, (int)items, size, s) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
   if (rows > 0x7FFFFFFFll || items > 0x7FFFFFFFll / (a.kv.cap / DEC_UNIT + 1)) return MK_ERR_UNSUPPORTED;
   if (launch(false, kv_decode_kernel<D, NT>, dim3(grid), DEC_THREADS, 0, s, a) != cudaSuccess)
     return MK_ERR_CUDA;

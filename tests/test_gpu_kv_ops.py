@@ -766,3 +766,46 @@ def test_outputs_that_overlap_or_name_the_queries_are_refused():
     assert torch.equal(c.cache.decode(one, c.lens), c.cache.decode(one.contiguous(), c.lens))
     cu = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
     assert torch.equal(c.cache.prefill(one, c.lens, cu), c.cache.prefill(one.contiguous(), c.lens, cu))
+
+
+def widened(c, rows=1 << 20):
+    """The same cache through a table that could name far longer sequences, as a
+    server's does: the choice of a kernel looks at what the table can hold."""
+    pages = max(c.table.shape[1], rows // c.block)
+    table = torch.full((c.table.shape[0], pages), -1, dtype=torch.int32, device="cuda")
+    table[:, :c.table.shape[1]] = c.table
+    return KVCache(c.k, c.v, table)
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("lens", LENS + [[2040, 3, 700], [130] * 40], ids=str)
+def test_decode_of_wide_tables(heads, lens):
+    c = Case(heads, lens, block=16, seed=58)
+    c.check("decode", c.run("decode"))
+    c.cache = widened(c)
+    c.check("decode", c.run("decode"))
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("heads", [(8, 2, 64), (32, 2, 128), (12, 1, 128), (33, 1, 64)])
+def test_decode_keeps_infinite_and_nan_values_to_their_dims(heads, wide):
+    c = Case(heads, [700, 65, 1], block=16, seed=59)
+    if wide:
+        c.cache = widened(c)
+    want, want_lse = c.run("decode")
+    ro, rl, A, err = c.reference()
+    for b, at, dim, value in ((0, 3, 7, math.inf), (0, 400, 9, math.nan), (1, 64, 0, -math.inf)):
+        blk, row = c.at(b, at, at + 1)
+        c.v[blk[0], 0, row[0], dim] = value
+    out, lse = c.run("decode")
+    assert torch.equal(lse[2], want_lse[2]) and torch.equal(out[2], want[2])
+    assert ((lse - want_lse).abs() <= 2.0 ** -18 * (1 + want_lse.abs()) + 2 * err).all()
+    g = c.hq // c.hkv
+    tol = 2.0 ** -8 * ro.abs() + (2 * err + 2.0 ** -14 + WEIGHT["decode"])[..., None] * A
+    ok = (out.double() - ro).abs() <= tol
+    spoilt = torch.zeros_like(ok)
+    spoilt[0, :g, 7] = spoilt[0, :g, 9] = spoilt[1, :g, 0] = True
+    assert ok[~spoilt].all()
+    assert (out[0, :g, 7] == math.inf).all() and torch.isnan(out[0, :g, 9]).all()
+    assert (out[1, :g, 0] == -math.inf).all()
+    c.cache.check()
