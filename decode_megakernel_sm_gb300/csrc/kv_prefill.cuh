@@ -1063,9 +1063,10 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
 // jobs of the parts from x + 1 on that begin inside the same job.  A warp has 32
 // rows, one per lane, and an eighth of the head's dimensions.
 template <int D>
-__global__ void __launch_bounds__(256) kv_prefill_join_kernel(const __grid_constant__ PfArgs p, int blocks) {
+__global__ void __launch_bounds__(256, 4) kv_prefill_join_kernel(const __grid_constant__ PfArgs p, int blocks) {
   using Sh = PfShape<D>;
   constexpr int N = D / 32;  // float4 pieces per warp
+  constexpr int F = 8 / N;   // states in flight
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const AttnArgs& a = p.a;
   const PfPart* parts = (const PfPart*)(a.ws + (size_t)blocks * 2 * Sh::STATE);
@@ -1076,20 +1077,22 @@ __global__ void __launch_bounds__(256) kv_prefill_join_kernel(const __grid_const
   if (!job.inside || (prev.inside && same(prev))) return;
   const int row = 32 * blockIdx.y + lane, tile = row >> 7, r = row & 127;
   const bool live = r < job.rows[tile];
+  if (r - lane >= job.rows[tile]) return;  // (the whole block)
   // The parts behind part i - 1, 32 at a time: how many begin inside the job, and
   // which of them hold anything.
   float m = -INFINITY, l = 0.f;
   float4 o[N];
 #pragma unroll
   for (int c = 0; c < N; c++) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  // Joins the states of up to four parts k0 + (bits of mask), all loads in flight at
-  // once; slot: of the first part's state.
+  // Joins the states of parts k0 + (bits of mask), the loads of F at a time in flight
+  // (four blocks to an SM; with 128-dim heads twice the loads and half the blocks took
+  // 4 us more); slot: of the first part's state.
   auto join = [&](int k0, unsigned mask, int slot) {
     while (mask) {
-      float mi[4], li[4];
-      float4 y[4][N];
+      float mi[F], li[F];
+      float4 y[F][N];
 #pragma unroll
-      for (int n = 0; n < 4; n++) {
+      for (int n = 0; n < F; n++) {
         const bool in = mask != 0 && live;
         const int k = k0 + (mask ? __ffs(mask) - 1 : 0);
         mask &= mask - 1;
@@ -1102,7 +1105,7 @@ __global__ void __launch_bounds__(256) kv_prefill_join_kernel(const __grid_const
                        : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
-      for (int n = 0; n < 4; n++) {
+      for (int n = 0; n < F; n++) {
         if (li[n] == 0.f) continue;  // no weight; o was not written
         const float top = fmaxf(m, mi[n]), f = join_weight(m, top), g = join_weight(mi[n], top);
         m = top;
