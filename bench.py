@@ -128,9 +128,10 @@ def step_bytes(cfg, positions, weight_bytes):
 
 
 def kernel_src_hash():
+    """Of the decode step's sources (kv_*: the cache operators, no part of a step)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "decode_megakernel_sm_gb300", "csrc")
-    for f in sorted(os.listdir(csrc)):
+    for f in sorted(f for f in os.listdir(csrc) if not f.startswith("kv_")):
         h.update(open(os.path.join(csrc, f), "rb").read())
     return h.hexdigest()[:16]
 
