@@ -12,22 +12,30 @@
 //               values one box per page piece, 128-byte swizzle); warp 0 also
 //               walks the block's piece of the line and posts one record per job
 //               in a ring, so that the others do no arithmetic on jobs
-//   warps 1, 3  issue the products of tile 0 and of tile 1: S_t = Q_t K^T and
-//               O_t += P_t V, both with the accumulator in tensor memory; P is the
-//               A operand straight from tensor memory, V the transposed (MN-major)
-//               B operand.  A warp each, so that neither tile waits for the other
+//   warps 1, 3  issue the products, S_t = Q_t K^T and O_t += P_t V for tile t, both
+//               with the accumulator in tensor memory; P is the A operand straight
+//               from tensor memory, V the transposed (MN-major) B operand
 //   warps 4-7   softmax of tile 0, one row per thread: S from tensor memory to
 //               registers, running maximum and sum in fp32, P (bf16) back to
 //               tensor memory; O's rescale, where a maximum rises by more than
 //               2^8 (rare after the first tiles), and the results
 //   warps 8-11  the same for tile 1
-// The two tiles take turns: the tensor cores work on one while the other's
-// softmax runs.  64-dim heads leave tensor memory for P beside S, so that the
-// next S is made while the softmax still works on this one; 128-dim heads fill
-// it (2 x 128 columns S, 2 x 128 O) and P takes S's place.
+// The tensor cores work on one tile while the other's softmax runs.  64-dim heads
+// leave tensor memory for P beside S, so that the next S, of the next job if need
+// be, is made while the softmax still works on this one; a warp per tile issues
+// their products, and neither tile waits for the other.  128-dim heads fill tensor
+// memory (2 x 128 columns S, 2 x 128 O): P takes S's place, its product starts when
+// half of it is there, and one warp issues both tiles' products in turn (a warp
+// each: 228 to 260 us where this took 223).
 //
-// Bound: with 128-dim heads the tensor cores (4 D operations a pair), with
-// 64-dim heads they and the exponentials alike.
+// Bound: with 128-dim heads the tensor cores (4 D operations a pair; 8192 tokens of
+// 16 heads, 275 GFLOP, take 183 us: 1.50 PFLOP/s, 0.78 of a measured GEMM's rate),
+// with 64-dim heads the softmax (8192 tokens of 32 heads: 267 us, 1.03 PFLOP/s).
+// A unit of two tiles has 32768 pairs: their exponentials take an SM 1040 cycles,
+// their scaling, sums, maxima and rounding as many on other pipes; the softmax warps
+// alone took 1625, with the products beside them about 2100.  Short prompts are
+// bound by the start (3 us of look-ups, 2.5 units a job) and the joins (5 of 87 us
+// for eight prompts of 512-2048 tokens).
 //
 // The line's measure is keys: a job costs its visible rows and PF_JOB_COST for
 // its start and end, and is cut wherever an equal share of the whole ends (or
