@@ -30,11 +30,11 @@
 //
 // Bound: with 128-dim heads the tensor cores (4 D operations a pair; 8192 tokens of
 // 16 heads, 275 GFLOP, take 183 us: 1.50 PFLOP/s, 0.78 of a measured GEMM's rate),
-// with 64-dim heads the softmax (8192 tokens of 32 heads: 267 us, 1.03 PFLOP/s).
+// with 64-dim heads the softmax (8192 tokens of 32 heads: 257 us, 1.07 PFLOP/s).
 // A unit of two tiles has 32768 pairs: their exponentials take an SM 1040 cycles,
 // their scaling, sums, maxima and rounding as many on other pipes; the softmax warps
 // alone took 1625, with the products beside them about 2100.  Short prompts are
-// bound by the start (3 us of look-ups, 2.5 units a job) and the joins (5 of 87 us
+// bound by the start (3 us of look-ups, 2.5 units a job) and the joins (5 of 84 us
 // for eight prompts of 512-2048 tokens).
 //
 // The line's measure is keys: a job costs its visible rows and PF_JOB_COST for
@@ -68,7 +68,9 @@ constexpr int PF_REGS = 168;      // per thread at launch (setmaxnreg deals them
 constexpr int PF_ROWS = 256;      // rows of a job
 constexpr int PF_UNIT = 128;      // cache rows of a unit
 constexpr int PF_JOB_COST = 320;  // a job's start and end, in keys (measured: 2.3 to 2.6 units)
-constexpr int PF_MIN_SHARE = 4 * PF_UNIT;  // a part of a job is not worth less
+// A part of a job is not worth less: a prompt of 1024 tokens, 8 kv heads of 64, 18.2 us
+// (a block per job) where 4 units take 20.9 (jobs cut and joined).
+constexpr int PF_MIN_SHARE = 7 * PF_UNIT;
 // A cut so many keys from a job's border moves there: a partial state and its join
 // cost about as much.
 constexpr int PF_SNAP = 4 * PF_UNIT;

@@ -809,3 +809,18 @@ def test_decode_keeps_infinite_and_nan_values_to_their_dims(heads, wide):
     assert (out[0, :g, 7] == math.inf).all() and torch.isnan(out[0, :g, 9]).all()
     assert (out[1, :g, 0] == -math.inf).all()
     c.cache.check()
+
+
+def test_batches_of_padding_alone():
+    # no sequence has a new token: nothing is written
+    c = Case((4, 2, 64), [40, 0], [3, 4], block=16, seed=60)
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    out = torch.full((7, 4, 64), 3.0, dtype=BF, device="cuda")
+    c.cache.prefill(c.q, c.lens, cu, out=out)
+    before = c.k.clone(), c.v.clone()
+    kv = torch.randn(7, 2, 64, device="cuda").to(BF)
+    c.cache.append(c.q, kv, kv, c.lens, cu, theta=1e4, q_out=out)
+    assert (out == 3).all()
+    for pool, was in zip((c.k, c.v), before):
+        assert torch.equal(pool.view(torch.int16), was.view(torch.int16))
+    c.cache.check()
