@@ -121,7 +121,7 @@ static int decode_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
 
-// The driver's tensor-map encoder, or nullptr.
+// The CUDA driver's tensor-map encoder, or nullptr.
 static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static const PFN_cuTensorMapEncodeTiled_v12000 enc = [] {
     PFN_cuTensorMapEncodeTiled_v12000 f = nullptr;
