@@ -45,7 +45,8 @@ class KVCache:
     kernels find in lens, cu and table (a length the cache cannot hold, offsets
     that fall, a block outside the pool) is kept for ``check``."""
 
-    __slots__ = ("k", "v", "table", "device", "heads", "dim", "held", "_index", "_view")
+    __slots__ = ("k", "v", "table", "device", "heads", "dim", "held", "_index", "_view", "_unusable",
+                 "__weakref__")
 
     def __init__(self, k, v, table=None):
         shape, device = k.shape, k.device
@@ -56,18 +57,28 @@ class KVCache:
             raise ValueError("k, v: expected contiguous tensors")
         if k.requires_grad or v.requires_grad:
             raise ValueError("k, v: the cache operators have no backward pass")
+        self.k, self.v, self.device, self._index = k, v, device, device.index
+        self._read_as(table, shape)
+
+    def _read_as(self, table, shape, unusable=None):
+        """Read the tensors through `table` from now on; unusable: why they cannot be
+        read so, for the calls to say."""
         n_blocks, self.heads, block, self.dim = shape
+        self._unusable = unusable
+        if unusable:
+            self.table, self.held, self._view = None, -1, None
+            return
         if table is None:
             self.held, tp, stride = n_blocks, 0, 0
         else:
-            if table.dtype is not _I32 or table.dim() != 2 or table.device != device or \
+            if table.dtype is not _I32 or table.dim() != 2 or table.device != self.device or \
                     not table.is_contiguous():
                 raise ValueError("table: expected a contiguous int32 matrix on the cache's device")
             self.held, stride = table.shape
             tp = table.data_ptr()
-        self.k, self.v, self.table, self.device, self._index = k, v, table, device, device.index
-        self._view = _VIEW.pack(k.data_ptr(), v.data_ptr(), n_blocks, self.heads, block, self.dim,
-                                tp, stride)
+        self.table = table
+        self._view = _VIEW.pack(self.k.data_ptr(), self.v.data_ptr(), n_blocks, self.heads, block,
+                                self.dim, tp, stride)
 
     # -- marshalling --------------------------------------------------------
     def _rows(self, t, name, dtype, n, heads):
@@ -100,6 +111,8 @@ class KVCache:
         lp = self._vector(lens, "lens", None)
         batch = lens.shape[0]
         if batch > self.held:
+            if self._unusable:
+                raise ValueError(self._unusable)
             raise ValueError(f"lens: {batch} sequences in a cache of {self.held}")
         if cu is None:
             if n != batch:

@@ -3,6 +3,7 @@ and marshals torch CUDA tensors to device pointers.  No arithmetic here."""
 from __future__ import annotations
 
 import ctypes as C
+import weakref
 
 import torch
 
@@ -81,6 +82,8 @@ class Decoder:
         self.weight_format = weight_format
         self.h = L.mk_create_ex(self.desc, w, kv, fmt)
         self.batch = 0
+        self._kv_block, self._kv_table = 0, None
+        self._views = weakref.WeakSet()  # what cache() handed out
 
     # -- schedule ---------------------------------------------------------
     def build_schedule(self, batch: int, max_ctx: int):
@@ -110,16 +113,41 @@ class Decoder:
         into the pools given at construction (block 0: back to contiguous)."""
         if block == 0:
             L.mk_set_kv_pages(self.h, 0, 0, None, 0)
-            self._kv_table = None
-            return
-        n_blocks = self.kcache[0].shape[0]
-        L.mk_set_kv_pages(self.h, block, n_blocks, _ptr(table, torch.int32), table.shape[1])
-        self._kv_table = table  # kept alive: the kernel reads it every step
+            table = None
+        else:
+            n_blocks = self.kcache[0].shape[0]
+            L.mk_set_kv_pages(self.h, block, n_blocks, _ptr(table, torch.int32), table.shape[1])
+        self._kv_block, self._kv_table = block, table  # kept alive: the kernel reads it every step
+        for view in list(self._views):
+            view._read_as(table, view.k.shape, self._unlike(view.k))
+
+    def _unlike(self, k):
+        """Why a layer's tensor does not show the cache as the handle reads it, or None."""
+        d = self.desc
+        if k.dim() != 4:
+            return f"expected 4-dimensional cache tensors, got {k.dim()} dimensions"
+        blocks, heads, rows, dim = k.shape
+        if self._kv_block:
+            want, ok = f"[n_blocks][{d.n_kv_heads}][{self._kv_block}][{d.head_dim}]", rows == self._kv_block
+        else:
+            want = f"[{d.max_batch}][{d.n_kv_heads}][{d.max_seq}][{d.head_dim}]"
+            ok = blocks >= d.max_batch and rows == d.max_seq
+        if ok and heads == d.n_kv_heads and dim == d.head_dim:
+            return None
+        return f"the handle reads its cache as {want}, the tensor is {list(k.shape)}" + \
+            ("" if self._kv_block else " (pools: call set_kv_pages first)")
 
     def cache(self, layer: int) -> KVCache:
         """Layer `layer`'s cache, contiguous or paged as the handle reads it, for the
-        cache operators: fill it from a prompt, attend to it, then step on."""
-        return KVCache(self.kcache[layer], self.vcache[layer], getattr(self, "_kv_table", None))
+        cache operators: fill it from a prompt, attend to it, then step on.  It follows
+        set_kv_pages; where the tensors are pools, that comes first.  (A captured graph
+        keeps the table it was captured with.)"""
+        why = self._unlike(self.kcache[layer])
+        if why:
+            raise ValueError(why)
+        view = KVCache(self.kcache[layer], self.vcache[layer], self._kv_table)
+        self._views.add(view)
+        return view
 
     def debug_read(self, what: str, layer: int):
         """An intermediate of the most recent step as a float32 numpy array:
