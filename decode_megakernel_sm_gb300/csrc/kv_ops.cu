@@ -209,6 +209,69 @@ static bool out_ok(const mk_rows* r, int n, int heads, int D) {
   return ts > hs ? hs >= D && ts >= hs * (heads - 1) + D : ts >= D && hs >= ts * (n - 1) + D;
 }
 
+// Where rows lie in memory, in bytes: n[0] x n[1] pieces of `size`, step[i] apart
+// (tokens, heads; steps that are not negative, none where there is one piece).
+using wide = __int128;
+struct Place {
+  wide at, size, n[2], step[2];
+  wide end() const { return at + (n[0] - 1) * step[0] + (n[1] - 1) * step[1] + size; }
+};
+
+static Place place(const void* p, wide bytes) { return {(wide)(uintptr_t)p, bytes, {1, 1}, {0, 0}}; }
+
+static Place place(const mk_rows* r, int n, int heads, int D, size_t size) {
+  Place x{(wide)(uintptr_t)r->p, (wide)D * size, {n, heads}, {r->token_stride, r->head_stride}};
+  for (int i = 0; i < 2; i++) {
+    x.step[i] *= size;
+    if (x.step[i] < 0) {
+      x.at += (x.n[i] - 1) * x.step[i];
+      x.step[i] = -x.step[i];
+    }
+    if (x.n[i] == 1 || x.step[i] == 0) {
+      x.n[i] = 1;
+      x.step[i] = 0;
+    }
+  }
+  return x;
+}
+
+// Whether [a, a + na) and [b, b + nb) are disjoint, all their shifts by the period too.
+static bool apart(wide a, wide na, wide b, wide nb, wide period) {
+  wide d = (b - a) % period;
+  if (d < 0) d += period;
+  return d >= na && d + nb <= period;
+}
+
+// Whether two places share no byte: one lies before the other, or both repeat with one
+// period (slices of one wider row) and their parts of it are apart, as wholes or, by
+// tokens, head by head.  False where that does not show it.
+static bool disjoint(const Place& x, const Place& y) {
+  if (x.end() <= y.at || y.end() <= x.at) return true;
+  for (int i = 0; i < 2; i++) {
+    const wide period = x.n[i] == 1 ? y.step[i] : x.step[i];
+    if (period == 0 || (x.n[i] > 1 && y.n[i] > 1 && x.step[i] != y.step[i])) continue;
+    const int o = 1 - i;
+    if (apart(x.at, (x.n[o] - 1) * x.step[o] + x.size, y.at, (y.n[o] - 1) * y.step[o] + y.size, period))
+      return true;
+    if (i == 1 || x.n[1] * y.n[1] > 1 << 14) continue;
+    bool all = true;
+    for (int j = 0; all && j < x.n[1]; j++)
+      for (int k = 0; all && k < y.n[1]; k++)
+        all = apart(x.at + j * x.step[1], x.size, y.at + k * y.step[1], y.size, period);
+    if (all) return true;
+  }
+  return false;
+}
+
+static bool same(const Place& x, const Place& y) {
+  return x.at == y.at && x.size == y.size && x.n[0] == y.n[0] && x.n[1] == y.n[1] &&
+         x.step[0] == y.step[0] && x.step[1] == y.step[1];
+}
+
+static Place pool(const mk_kv_view* kv, const void* p) {
+  return place(p, (wide)kv->n_blocks * kv->n_kv_heads * kv->block * kv->head_dim * 2);
+}
+
 static Rows rows(const mk_rows* r) { return Rows{r->p, r->token_stride, r->head_stride}; }
 
 // Fills the device structs; MK_OK, or why not.
@@ -257,6 +320,17 @@ extern "C" int mk_kv_append(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q
   if (!rows_ok(k, size) || !rows_ok(v, size) ||
       (n_q_heads > 0 && (!rows_ok(q, size) || !out_ok(q_out, bt->n_tokens, n_q_heads, kv->head_dim))))
     return MK_ERR_INVALID_ARG;
+  // What is written may not be read or written by another thread's piece: queries turn
+  // in place (a thread reads its pieces before it writes them) or go elsewhere.
+  const int n = bt->n_tokens, D = kv->head_dim;
+  const Place kp = pool(kv, kv->k), vp = pool(kv, kv->v);
+  if (!disjoint(kp, vp)) return MK_ERR_INVALID_ARG;
+  if (n_q_heads > 0) {
+    const Place to = place(q_out, n, n_q_heads, D, 2), from = place(q, n, n_q_heads, D, size);
+    if (!(same(to, from) || disjoint(to, from)) || !disjoint(to, place(k, n, kv->n_kv_heads, D, size)) ||
+        !disjoint(to, place(v, n, kv->n_kv_heads, D, size)) || !disjoint(to, kp) || !disjoint(to, vp))
+      return MK_ERR_INVALID_ARG;
+  }
   a.k = rows(k);
   a.v = rows(v);
   if (n_q_heads > 0) {
@@ -267,7 +341,6 @@ extern "C" int mk_kv_append(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q
   }
   a.Hq = n_q_heads;
   a.rotate = rope_theta != 0.0;
-  const int D = kv->head_dim;
   if (a.rotate) {
     // theta^(-2t/D) / 2 pi as a fraction of 2^64, from the powers of two of t
     double pw[6];
@@ -323,12 +396,25 @@ static int attention(bool decode, const mk_kv_view* kv, const mk_kv_batch* bt, i
   if (!std::isfinite(scale) || !rows_ok(q, 2) ||
       !out_ok(out, bt->n_tokens, n_q_heads, kv->head_dim) || (d_lse && !aligned(d_lse, 4)))
     return MK_ERR_INVALID_ARG;
-  if (out->p == q->p) return MK_ERR_INVALID_ARG;  // q is read again after out is written
+  // other blocks, and rows that are redone, read q and the cache after out is written
+  const Place to = place(out, bt->n_tokens, n_q_heads, kv->head_dim, 2),
+              from = place(q, bt->n_tokens, n_q_heads, kv->head_dim, 2),
+              lse = place(d_lse, d_lse ? (wide)bt->n_tokens * n_q_heads * 4 : 0);
+  const Place kp = pool(kv, kv->k), vp = pool(kv, kv->v);
+  if (!disjoint(to, from) || !disjoint(to, kp) || !disjoint(to, vp)) return MK_ERR_INVALID_ARG;
+  if (d_lse && !(disjoint(lse, from) && disjoint(lse, to) && disjoint(lse, kp) && disjoint(lse, vp)))
+    return MK_ERR_INVALID_ARG;
   size_t need = 0;
   const int wrc = mk_attn_workspace_bytes(decode, bt->n_tokens, bt->batch, n_q_heads,
                                           kv->n_kv_heads, kv->head_dim, &need);
   if (wrc) return wrc;
-  if (need > 0 && (!d_ws || !aligned(d_ws, 256) || ws_bytes < need)) return MK_ERR_INVALID_ARG;
+  if (need > 0) {
+    if (!d_ws || !aligned(d_ws, 256) || ws_bytes < need) return MK_ERR_INVALID_ARG;
+    const Place ws = place(d_ws, need);
+    if (!(disjoint(ws, from) && disjoint(ws, to) && disjoint(ws, kp) && disjoint(ws, vp)) ||
+        (d_lse && !disjoint(ws, lse)))
+      return MK_ERR_INVALID_ARG;
+  }
   a.q = rows(q);
   a.o = rows(out);
   a.lse = d_lse;

@@ -244,9 +244,13 @@ typedef struct {
  * of p * f_t, as in the decode step; arithmetic in fp32, angles exact to fp32
  * at any position, one rounding to bf16.  rope_theta 0: no rotation; else >= 1.
  * src_type: the type of q, k and v, MK_SRC_BF16 or MK_SRC_F32.  q_out (bf16)
- * receives the rotated queries; it may be q itself (bf16).  n_q_heads 0:
- * there are none, q and q_out are ignored.  Two new tokens that name the same
- * cache row (through a table that repeats a block) race.                   */
+ * receives the rotated queries; it may be q itself (bf16, the same strides) and
+ * shares no memory with q, k, v or the cache otherwise, nor k's pool with v's
+ * (MK_ERR_INVALID_ARG; rows that interleave with others pass where both have the
+ * same stride between tokens, or between heads).  n_q_heads 0: there are none, q
+ * and q_out are ignored.  Two new tokens that name the same cache row (through a
+ * table that repeats a block) race, and so do sources that are cache rows which
+ * the call writes.                                                         */
 #define MK_SRC_BF16 0
 #define MK_SRC_F32 1
 int mk_kv_append(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q_heads, const mk_rows* q,
@@ -266,7 +270,8 @@ int mk_kv_append(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q_heads, con
  *   mk_attn_prefill: any number of new tokens per sequence, causal.  At most
  *     128 query heads per kv head, and pools of less than 2^31 rows
  *     (n_blocks * n_kv_heads * block).
- * scale is finite; out is not q.  A call whose work cannot be numbered in 31
+ * scale is finite.  out, d_lse and d_ws share no memory with one another, q or the
+ * cache (MK_ERR_INVALID_ARG; interleaved rows as above).  A call whose work cannot be numbered in 31
  * bits (decode: batch * n_q_heads, or items of 64 rows when every sequence has
  * all the rows that the view can hold) is MK_ERR_UNSUPPORTED.
  * d_ws: device scratch of at least mk_attn_workspace_bytes() bytes, 256-byte

@@ -1,0 +1,151 @@
+"""The cache operators' host code over a stand-in for the CUDA runtime: which calls are
+launched, which are refused, and what becomes of the runtime's errors."""
+import shutil
+
+import pytest
+
+from decode_megakernel_sm_gb300 import _lib as L
+from tests.kv_fake import Fake
+
+pytestmark = pytest.mark.skipif(not (shutil.which("nvcc") and shutil.which("g++")),
+                                reason="builds the host code")
+
+G = 1 << 30
+K, V, TABLE, LENS, CU, WS, FREE = (G * i for i in range(1, 8))  # addresses far apart
+
+
+@pytest.fixture(scope="module")
+def built():
+    return Fake()
+
+
+@pytest.fixture
+def fake(built):
+    built.lib.fake_reset()
+    return built
+
+
+def view(**kw):
+    a = dict(k=K, v=V, n_blocks=8, n_kv_heads=2, block=16, head_dim=64, d_table=TABLE, table_stride=4)
+    a.update(kw)
+    return L.mk_kv_view(*[a[n] for n, _ in L.mk_kv_view._fields_])
+
+
+POOL = 8 * 2 * 16 * 64 * 2  # bytes of the view's pools
+
+
+def batch(n=7, batch=2, cu=CU):
+    return L.mk_kv_batch(batch, n, LENS, cu)
+
+
+def rows(p=FREE, ts=256, hs=64):
+    return L.mk_rows(p, ts, hs)
+
+
+def append(fake, q=None, k=None, v=None, qo=None, src=L.MK_SRC_BF16, kv=None, hq=4, n=7, theta=1e4):
+    return fake.lib.mk_kv_append(kv or view(), batch(n), hq, q or rows(), k or rows(FREE + 4 * G),
+                                 v or rows(FREE + 5 * G), src, qo or rows(FREE + G), theta, None)
+
+
+def attn(fake, kind, q=None, out=None, lse=None, ws=WS, n=7, hq=4, scale=0.125, kv=None):
+    decode = kind == "decode"
+    bt = batch(2 if decode else n, cu=None if decode else CU)
+    return getattr(fake.lib, f"mk_attn_{kind}")(kv or view(), bt, hq, q or rows(), scale,
+                                                out or rows(FREE + G), lse, ws, 1 << 28, None)
+
+
+KINDS = ["decode", "prefill"]
+# q and out as [n][4][64] bf16 in one buffer, out at a distance: rows that share memory
+SHARING = {
+    "shifted by a token": (rows(), rows(FREE + 512)),
+    "shifted by half a token": (rows(), rows(FREE + 256)),
+    "before it": (rows(FREE + 512), rows(FREE)),
+    "slices that meet": (rows(ts=512), rows(FREE + 3 * 128, ts=512)),
+    "interleaved heads that meet": (rows(ts=512, hs=128), rows(FREE + 128 + 64, ts=512, hs=128)),
+    "other strides": (rows(), rows(FREE, ts=512, hs=64)),
+    "heads first": (rows(ts=64, hs=448), rows(FREE + 128, ts=64, hs=448)),
+    "one row for all": (rows(FREE + 512, ts=0), rows(FREE)),
+}
+APART = {
+    "far apart": (rows(), rows(FREE + G)),
+    "end to end": (rows(), rows(FREE + 7 * 512)),
+    "slices of one row": (rows(ts=512), rows(FREE + 512, ts=512)),
+    "slices the other way": (rows(FREE + 512, ts=512), rows(ts=512)),
+    "heads in turn": (rows(ts=512, hs=128), rows(FREE + 128, ts=512, hs=128)),
+    "heads first in turn": (rows(ts=64, hs=1024), rows(FREE + 1024, ts=64, hs=1024)),
+    "heads in turn, one in four": (rows(ts=1024, hs=128), rows(FREE + 128, ts=1024, hs=256)),
+    "one row for all": (rows(FREE + 8192, ts=0), rows(FREE)),
+}
+
+
+@pytest.mark.parametrize("name", SHARING)
+def test_outputs_that_share_memory_with_the_queries_are_refused(fake, name):
+    q, out = SHARING[name]
+    for kind in KINDS:
+        assert attn(fake, kind, q=q, out=out) == L.MK_ERR_INVALID_ARG
+    if name != "one row for all":
+        assert append(fake, q=q, qo=out) == L.MK_ERR_INVALID_ARG
+    assert fake.launches() == []
+
+
+@pytest.mark.parametrize("name", APART)
+def test_outputs_beside_the_queries_are_taken(fake, name):
+    q, out = APART[name]
+    for kind in KINDS:
+        assert attn(fake, kind, q=q, out=out) == L.MK_OK
+    assert append(fake, q=q, qo=out) == L.MK_OK
+    assert len(fake.launches()) >= 4
+
+
+def test_queries_turn_in_place(fake):
+    for r in (rows(), rows(ts=512), rows(ts=64, hs=1024)):
+        assert append(fake, q=r, qo=r) == L.MK_OK
+    # the same rows, read as fp32 or in another order
+    assert append(fake, q=rows(), qo=rows(), src=L.MK_SRC_F32) == L.MK_ERR_INVALID_ARG
+    assert append(fake, q=rows(ts=256, hs=64), qo=rows(ts=64, hs=448)) == L.MK_ERR_INVALID_ARG
+
+
+def test_append_in_a_fused_projection(fake):
+    # [n][4 + 2 + 2][64]: queries in place, keys and values beside them
+    def part(i):
+        return rows(FREE + 128 * i, ts=512)
+    assert append(fake, q=part(0), qo=part(0), k=part(4), v=part(6)) == L.MK_OK
+    assert append(fake, q=part(0), qo=part(2), k=part(4), v=part(6)) == L.MK_ERR_INVALID_ARG
+    assert append(fake, q=rows(FREE + 2 * G), qo=part(4), k=part(4), v=part(6)) == L.MK_ERR_INVALID_ARG
+    assert append(fake, q=rows(FREE + 2 * G), qo=part(2), k=part(4), v=part(6)) == L.MK_ERR_INVALID_ARG
+    assert append(fake, n=1, q=part(0), qo=part(0), k=part(4), v=part(6)) == L.MK_OK
+
+
+@pytest.mark.parametrize("at", [K, V, K + POOL - 256, V - 512])
+def test_outputs_in_the_cache_are_refused(fake, at):
+    for kind in KINDS:
+        assert attn(fake, kind, out=rows(at)) == L.MK_ERR_INVALID_ARG
+        assert attn(fake, kind, lse=at) == (L.MK_ERR_INVALID_ARG if at != V - 512 else L.MK_OK)
+    assert append(fake, qo=rows(at)) == L.MK_ERR_INVALID_ARG
+
+
+def test_outputs_at_the_cache_are_taken(fake):
+    assert attn(fake, "prefill", out=rows(K + POOL)) == L.MK_OK
+    assert attn(fake, "prefill", out=rows(K - 7 * 512)) == L.MK_OK
+    assert attn(fake, "decode", lse=K + POOL) == L.MK_OK
+    # keys that are their own values are read, not written
+    assert attn(fake, "decode", kv=view(v=K)) == L.MK_OK
+    assert append(fake, kv=view(v=K)) == L.MK_ERR_INVALID_ARG
+    assert append(fake, kv=view(v=K + POOL - 256)) == L.MK_ERR_INVALID_ARG
+    assert append(fake, kv=view(v=K + POOL)) == L.MK_OK
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_scratch_and_lse_share_nothing(fake, kind):
+    for ws in (FREE, FREE + G, K, V - 256, FREE + 2 * G):
+        assert attn(fake, kind, ws=ws, lse=FREE + 2 * G) == L.MK_ERR_INVALID_ARG
+    for lse in (FREE, FREE + G):
+        assert attn(fake, kind, lse=lse) == L.MK_ERR_INVALID_ARG
+    assert fake.launches() == []
+    assert attn(fake, kind, lse=FREE + 2 * G) == L.MK_OK
+
+
+def test_strides_of_any_size(fake):
+    assert attn(fake, "decode", q=rows(FREE + G, ts=1 << 62), out=rows()) == L.MK_OK
+    assert attn(fake, "decode", q=rows(ts=-256)) == L.MK_OK
+    assert attn(fake, "decode", q=rows(FREE + 512, ts=-256), out=rows(FREE)) == L.MK_ERR_INVALID_ARG
