@@ -94,14 +94,19 @@ MK_DEV void kv_new_tokens(const KvBatch& bt, int b, int& first, int& n) {
 
 // Sequence that new token t belongs to (batch: none, a padding row), found by
 // one warp: the number of sequences that end at or before t.  All lanes call.
+// Reports offsets that fall or leave the rows, whichever sequence has them.
 MK_DEV int kv_seq_of_token(const KvBatch& bt, int t, int lane) {
   if (!bt.cu) return t;
   int b = 0;
+  bool bad = false;
   for (int i0 = 0; i0 < bt.batch; i0 += 32) {
     const int i = i0 + lane;
-    const bool before = i < bt.batch && __ldg(bt.cu + i + 1) <= t;
-    b += __popc(__ballot_sync(0xFFFFFFFFu, before));
+    const bool in = i < bt.batch;
+    const int from = in ? __ldg(bt.cu + i) : 0, to = in ? __ldg(bt.cu + i + 1) : 0;
+    bad |= from < 0 || to < from || to > bt.n_tokens;
+    b += __popc(__ballot_sync(0xFFFFFFFFu, in && to <= t));
   }
+  if (bad) kv_fail(MK_ERR_INVALID_ARG);
   return b;
 }
 
