@@ -281,7 +281,8 @@ static int check(const mk_kv_view* kv, const mk_kv_batch* bt, KvView& v, KvBatch
       kv->n_kv_heads < 1 || kv->block < 1)
     return MK_ERR_INVALID_ARG;
   if (bt->batch < 0 || bt->n_tokens < 0 || (bt->batch > 0 && !bt->d_lens) ||
-      (!bt->d_cu && bt->n_tokens != bt->batch))
+      (!bt->d_cu && bt->n_tokens != bt->batch) || !aligned(bt->d_lens, 4) || !aligned(bt->d_cu, 4) ||
+      !aligned(kv->d_table, 4))
     return MK_ERR_INVALID_ARG;
   int shift = 0;
   if (kv->d_table) {

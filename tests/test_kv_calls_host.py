@@ -149,3 +149,21 @@ def test_strides_of_any_size(fake):
     assert attn(fake, "decode", q=rows(FREE + G, ts=1 << 62), out=rows()) == L.MK_OK
     assert attn(fake, "decode", q=rows(ts=-256)) == L.MK_OK
     assert attn(fake, "decode", q=rows(FREE + 512, ts=-256), out=rows(FREE)) == L.MK_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("by", [1, 2, 3])
+def test_vectors_off_their_alignment_are_refused(fake, by):
+    """A kernel that loads an int off its 4-byte boundary faults."""
+    for bt in (L.mk_kv_batch(2, 7, LENS + by, CU), L.mk_kv_batch(2, 7, LENS, CU + by)):
+        assert fake.lib.mk_kv_append(view(), bt, 4, rows(), rows(FREE + 4 * G), rows(FREE + 5 * G), 0,
+                                     rows(FREE + G), 1e4, None) == L.MK_ERR_INVALID_ARG
+        assert fake.lib.mk_attn_prefill(view(), bt, 4, rows(), 0.125, rows(FREE + G), None, WS, 1 << 28,
+                                        None) == L.MK_ERR_INVALID_ARG
+    assert fake.lib.mk_attn_decode(view(), L.mk_kv_batch(2, 2, LENS + by, None), 4, rows(), 0.125,
+                                   rows(FREE + G), None, WS, 1 << 28, None) == L.MK_ERR_INVALID_ARG
+    odd = view(d_table=TABLE + by)
+    assert append(fake, kv=odd) == L.MK_ERR_INVALID_ARG
+    for kind in KINDS:
+        assert attn(fake, kind, kv=odd) == L.MK_ERR_INVALID_ARG
+        assert attn(fake, kind, lse=FREE + 2 * G + by) == L.MK_ERR_INVALID_ARG
+    assert fake.launches() == []
