@@ -394,7 +394,7 @@ static int attention(bool decode, const mk_kv_view* kv, const mk_kv_batch* bt, i
   if ((bt->d_cu != nullptr) == decode) return MK_ERR_INVALID_ARG;
   if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads) return MK_ERR_INVALID_ARG;
   if (bt->n_tokens == 0 || bt->batch == 0) return MK_OK;
-  if (!std::isfinite(scale) || !rows_ok(q, 2) ||
+  if (!std::isfinite(scale * LOG2E) || !rows_ok(q, 2) ||
       !out_ok(out, bt->n_tokens, n_q_heads, kv->head_dim) || (d_lse && !aligned(d_lse, 4)))
     return MK_ERR_INVALID_ARG;
   // other blocks, and rows that are redone, read q and the cache after out is written

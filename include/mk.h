@@ -270,7 +270,7 @@ int mk_kv_append(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q_heads, con
  *   mk_attn_prefill: any number of new tokens per sequence, causal.  At most
  *     128 query heads per kv head, and pools of less than 2^31 rows
  *     (n_blocks * n_kv_heads * block).
- * scale is finite.  out, d_lse and d_ws share no memory with one another, q or the
+ * scale and scale * log2 e are finite.  out, d_lse and d_ws share no memory with one another, q or the
  * cache (MK_ERR_INVALID_ARG; interleaved rows as above).  A call whose work cannot be numbered in 31
  * bits (decode: batch * n_q_heads, or items of 64 rows when every sequence has
  * all the rows that the view can hold) is MK_ERR_UNSUPPORTED.

@@ -167,3 +167,12 @@ def test_vectors_off_their_alignment_are_refused(fake, by):
         assert attn(fake, kind, kv=odd) == L.MK_ERR_INVALID_ARG
         assert attn(fake, kind, lse=FREE + 2 * G + by) == L.MK_ERR_INVALID_ARG
     assert fake.launches() == []
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("scale", [2.5e38, -2.5e38, 3.4e38])
+def test_scales_that_overflow_in_powers_of_two_are_refused(fake, kind, scale):
+    # the kernels work with scale * log2 e: infinite, it makes a score of 0 NaN
+    assert attn(fake, kind, scale=scale) == L.MK_ERR_INVALID_ARG
+    assert fake.launches() == []
+    assert attn(fake, kind, scale=2.3e38 if scale > 0 else -2.3e38) == L.MK_OK
