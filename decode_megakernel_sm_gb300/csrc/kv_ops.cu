@@ -15,6 +15,13 @@
 
 namespace mk {
 
+// A failed runtime call: its error is this call's status, and none of a later call.
+static int cuda_failed() {
+  cudaGetLastError();
+  return MK_ERR_CUDA;
+}
+static int status_of(cudaError_t e) { return e == cudaSuccess ? MK_OK : cuda_failed(); }
+
 // Streaming multiprocessors of the current device, 0 on an error.
 static int sm_count() {
   int dev = 0, n = 0;
@@ -46,11 +53,11 @@ static cudaError_t launch(bool early, void (*kernel)(P...), dim3 grid, unsigned 
 // with one, 9833 tokens of 48 heads of 64); one token to a block starts sooner (3.2 us
 // against 4.1 for a single token), so few tokens take that.
 template <int D, bool F32>
-static void append_launch(const AppendArgs& a, int n_sm, cudaStream_t s) {
+static cudaError_t append_launch(const AppendArgs& a, int n_sm, cudaStream_t s) {
   constexpr int NT = KV_APPEND_TOKENS;
   const int n = a.bt.n_tokens;
-  if (n <= NT * n_sm) launch(false, kv_append_kernel<D, F32, 1>, dim3(n), KV_APPEND_THREADS, 0, s, a);
-  else launch(false, kv_append_kernel<D, F32, NT>, dim3((n + NT - 1) / NT), KV_APPEND_THREADS, 0, s, a);
+  if (n <= NT * n_sm) return launch(false, kv_append_kernel<D, F32, 1>, dim3(n), KV_APPEND_THREADS, 0, s, a);
+  return launch(false, kv_append_kernel<D, F32, NT>, dim3((n + NT - 1) / NT), KV_APPEND_THREADS, 0, s, a);
 }
 
 // Query heads of one item of the decode kernel: 8 fill half of a tensor-core
@@ -108,17 +115,15 @@ static int decode_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
   const long long rows = (long long)a.bt.batch * a.Hq;
   const long long items = (long long)a.bt.batch * a.kv.Hkv * ((a.G + Sh::HB - 1) / Sh::HB);
   if (const int size = cluster_size(items, grid, a.kv.cap))
-    return cluster_launch<D, NT>(a, (int)items, size, s) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+    return status_of(cluster_launch<D, NT>(a, (int)items, size, s));
   if (rows > 0x7FFFFFFFll || items > 0x7FFFFFFFll / (a.kv.cap / DEC_UNIT + 1)) return MK_ERR_UNSUPPORTED;
   if (launch(false, kv_decode_kernel<D, NT>, dim3(grid), DEC_THREADS, 0, s, a) != cudaSuccess)
-    return MK_ERR_CUDA;
+    return cuda_failed();
   // Warps per row of the join: where items are few, each is split into many states
   // (about grid / items): 8 items of 32768 rows 18.9 us with eight warps, 20.0 with
   // four; 256 items of 512-2048 rows 24.0 with eight, 21.3 with four.
-  const cudaError_t e = items <= grid / 16 ? join_launch<D, NT, 8>(a, grid, rows, s)
-                                           : join_launch<D, NT, 4>(a, grid, rows, s);
-  if (e != cudaSuccess) return MK_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+  return status_of(items <= grid / 16 ? join_launch<D, NT, 8>(a, grid, rows, s)
+                                      : join_launch<D, NT, 4>(a, grid, rows, s));
 }
 
 // The CUDA driver's tensor-map encoder, or nullptr.
@@ -157,7 +162,7 @@ static bool prefill_ready() {
 template <int D>
 static int prefill_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
   const auto enc = tensor_map_encoder();
-  if (!enc || !prefill_ready<D>()) return MK_ERR_CUDA;
+  if (!enc || !prefill_ready<D>()) return cuda_failed();
   const long long rows = (long long)a.kv.n_blocks * a.kv.Hkv * a.kv.block;
   if (rows >= 0x7FFFFFFFll) return MK_ERR_UNSUPPORTED;
   PfArgs p{};
@@ -188,8 +193,8 @@ static int prefill_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
              maps[1], maps[2]) != cudaSuccess ||
       (n_sm > 1 && launch(true, kv_prefill_join_kernel<D>, dim3(n_sm - 1, PF_ROWS / 32), 256, 0, s, p,
                           n_sm) != cudaSuccess))
-    return MK_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+    return cuda_failed();
+  return MK_OK;
 }
 
 // ------------------------------------------------------- argument checks ----
@@ -301,8 +306,6 @@ static int check(const mk_kv_view* kv, const mk_kv_batch* bt, KvView& v, KvBatch
   return MK_OK;
 }
 
-static int launched() { return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA; }
-
 }  // namespace mk
 
 using namespace mk;
@@ -354,16 +357,10 @@ extern "C" int mk_kv_append(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q
     }
   }
   const int n_sm = sm_count();
-  if (n_sm == 0) return MK_ERR_CUDA;
+  if (n_sm == 0) return cuda_failed();
   cudaStream_t s = (cudaStream_t)stream;
-  if (D == 64) {
-    if (size == 4) append_launch<64, true>(a, n_sm, s);
-    else append_launch<64, false>(a, n_sm, s);
-  } else {
-    if (size == 4) append_launch<128, true>(a, n_sm, s);
-    else append_launch<128, false>(a, n_sm, s);
-  }
-  return launched();
+  if (D == 64) return status_of(size == 4 ? append_launch<64, true>(a, n_sm, s) : append_launch<64, false>(a, n_sm, s));
+  return status_of(size == 4 ? append_launch<128, true>(a, n_sm, s) : append_launch<128, false>(a, n_sm, s));
 }
 
 extern "C" int mk_attn_workspace_bytes(int decode, int n_tokens, int batch, int n_q_heads,
@@ -374,7 +371,7 @@ extern "C" int mk_attn_workspace_bytes(int decode, int n_tokens, int batch, int 
   if (head_dim != 64 && head_dim != 128) return MK_ERR_UNSUPPORTED;
   *bytes = 0;
   const int n = sm_count(), nt = decode_tiles(n_q_heads / n_kv_heads);
-  if (n == 0) return MK_ERR_CUDA;
+  if (n == 0) return cuda_failed();
   if (!decode) {
     *bytes = ((head_dim == 64 ? PfShape<64>::STATE : PfShape<128>::STATE) * sizeof(float) * 2 +
               sizeof(PfPart)) * n;
@@ -453,11 +450,11 @@ extern "C" int mk_kv_status(void* stream) {
   if (cudaMemcpyFromSymbolAsync(&word, kv_status_word, sizeof(int), 0, cudaMemcpyDeviceToHost, s) !=
           cudaSuccess ||
       cudaStreamSynchronize(s) != cudaSuccess)
-    return MK_ERR_CUDA;
+    return cuda_failed();
   if (word != 0 &&
       (cudaMemcpyToSymbolAsync(kv_status_word, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) !=
            cudaSuccess ||
        cudaStreamSynchronize(s) != cudaSuccess))
-    return MK_ERR_CUDA;
+    return cuda_failed();
   return word;
 }

@@ -176,3 +176,55 @@ def test_scales_that_overflow_in_powers_of_two_are_refused(fake, kind, scale):
     assert attn(fake, kind, scale=scale) == L.MK_ERR_INVALID_ARG
     assert fake.launches() == []
     assert attn(fake, kind, scale=2.3e38 if scale > 0 else -2.3e38) == L.MK_OK
+
+
+# ---- the runtime's errors ----
+WIDE = dict(table_stride=1 << 16)  # decode takes two launches for tables like this
+CALLS = {
+    "append": (append, 1, {}),
+    "decode by clusters": (attn, 1, dict(kind="decode")),
+    "decode by the line": (attn, 2, dict(kind="decode", kv=view(**WIDE))),
+    "prefill": (attn, 2, dict(kind="prefill")),
+    "prefill of 128 dims": (attn, 2, dict(kind="prefill", kv=view(head_dim=128), q=rows(ts=512, hs=128),
+                                          out=rows(FREE + G, ts=512, hs=128))),
+}
+INVALID_VALUE, OUT_OF_MEMORY = 1, 2
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_failed_launch_is_its_own_calls_error(fake, name):
+    call, launches, kw = CALLS[name]
+    for i in range(launches):
+        fake.lib.fake_reset()
+        fake.fail("launch", after=i)
+        assert call(fake, **kw) == L.MK_ERR_CUDA
+        assert fake.lib.fake_peek() == 0  # nothing left for the next call to find
+        assert len(fake.launches()) == i
+        assert call(fake, **kw) == L.MK_OK
+        assert len(fake.launches()) == i + launches
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_an_error_of_another_call_is_not_reported(fake, name):
+    call, launches, kw = CALLS[name]
+    fake.lib.fake_pending(OUT_OF_MEMORY)
+    assert call(fake, **kw) == L.MK_OK
+    assert len(fake.launches()) == launches
+
+
+@pytest.mark.parametrize("failing", ["device", "attribute"])
+@pytest.mark.parametrize("name", CALLS)
+def test_failed_queries_launch_nothing_and_leave_nothing(fake, name, failing):
+    call, launches, kw = CALLS[name]
+    fake.fail(failing, error=INVALID_VALUE)
+    assert call(fake, **kw) == L.MK_ERR_CUDA
+    assert fake.launches() == [] and fake.lib.fake_peek() == 0
+    assert call(fake, **kw) == L.MK_OK
+
+
+@pytest.mark.parametrize("failing", ["copy", "sync"])
+def test_a_failed_status_leaves_nothing(fake, failing):
+    fake.fail(failing)
+    assert fake.lib.mk_kv_status(None) == L.MK_ERR_CUDA
+    assert fake.lib.fake_peek() == 0
+    assert fake.lib.mk_kv_status(None) == L.MK_OK
