@@ -231,8 +231,10 @@ class KVCache:
 
     def check(self, stream=None):
         """Wait for the stream and raise MkError if a kernel of any cache operator on
-        this device has found bad contents (or run into a time limit) since the last
-        check."""
+        this device, of whichever cache, thread or stream, has run into a time limit
+        (MK_ERR_TIMEOUT) or found bad contents (MK_ERR_INVALID_ARG) since the last
+        check.  One check answers for all of them: a program with several users of a
+        device checks in one place."""
         def call(raw):
             status = L.mk_kv_status(raw)
             if status != L.MK_OK:

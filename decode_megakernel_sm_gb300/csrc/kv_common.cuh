@@ -13,11 +13,16 @@ namespace mk {
 MK_DEV void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
 MK_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// What the operators found since mk_kv_status() last looked (MK_OK or an
-// MK_ERR_* code; the first finding stays).
-__device__ int kv_status_word = 0;
+// What the operators found since mk_kv_status() last looked, as bits, and what it took.
+constexpr int KV_FOUND_CONTENTS = 1, KV_FOUND_TIMEOUT = 2;
+__device__ int kv_status_word = 0, kv_status_taken = 0;
 
-MK_DEV void kv_fail(int code) { atomicCAS(&kv_status_word, 0, code); }
+MK_DEV void kv_fail(int code) {
+  atomicOr(&kv_status_word, code == MK_ERR_TIMEOUT ? KV_FOUND_TIMEOUT : KV_FOUND_CONTENTS);
+}
+
+// Takes and clears in one step: kernels on other streams may add to the word meanwhile.
+__global__ void kv_status_take() { kv_status_taken = atomicExch(&kv_status_word, 0); }
 
 // Two floats rounded to bf16, the first in the low half.
 MK_DEV uint32_t bf2(float lo, float hi) {

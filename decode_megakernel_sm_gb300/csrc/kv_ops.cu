@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdlib>
 #include <limits>
+#include <mutex>
 
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -445,16 +446,15 @@ extern "C" int mk_attn_prefill(const mk_kv_view* kv, const mk_kv_batch* bt, int 
 
 extern "C" int mk_kv_status(void* stream) {
   cudaStream_t s = (cudaStream_t)stream;
-  int word = 0;
-  const int zero = 0;
-  if (cudaMemcpyFromSymbolAsync(&word, kv_status_word, sizeof(int), 0, cudaMemcpyDeviceToHost, s) !=
+  // (the caller's work outside the lock: it may take long, or wait for another thread)
+  if (cudaStreamSynchronize(s) != cudaSuccess) return cuda_failed();
+  static std::mutex one_at_a_time;  // kv_status_taken is one per device
+  std::lock_guard<std::mutex> guard(one_at_a_time);
+  int found = 0;
+  if (launch(false, kv_status_take, dim3(1), 1, 0, s) != cudaSuccess ||
+      cudaMemcpyFromSymbolAsync(&found, kv_status_taken, sizeof(int), 0, cudaMemcpyDeviceToHost, s) !=
           cudaSuccess ||
       cudaStreamSynchronize(s) != cudaSuccess)
     return cuda_failed();
-  if (word != 0 &&
-      (cudaMemcpyToSymbolAsync(kv_status_word, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) !=
-           cudaSuccess ||
-       cudaStreamSynchronize(s) != cudaSuccess))
-    return cuda_failed();
-  return word;
+  return found & KV_FOUND_TIMEOUT ? MK_ERR_TIMEOUT : found ? MK_ERR_INVALID_ARG : MK_OK;
 }

@@ -290,9 +290,12 @@ int mk_attn_prefill(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q_heads, 
 int mk_attn_workspace_bytes(int decode, int n_tokens, int batch, int n_q_heads, int n_kv_heads,
                             int head_dim, size_t* bytes);
 
-/* Wait for `stream`, then return and clear what the KV-cache operators found
- * on the current device since the last call (MK_OK, MK_ERR_INVALID_ARG or
- * MK_ERR_TIMEOUT); one word for all streams.  Not during a capture.        */
+/* Wait for `stream`, then return and clear, in one step, what the KV-cache
+ * operators found on the current device since the last call: MK_ERR_TIMEOUT if
+ * any call gave up, else MK_ERR_INVALID_ARG if any found bad contents, else
+ * MK_OK.  One word for all streams and callers: whoever asks answers for all
+ * calls on the device, and passes a finding on to the others.  Not during a
+ * capture.                                                                 */
 int mk_kv_status(void* stream);
 
 /* Diagnostics: an intermediate of the handle's most recent step

@@ -24,7 +24,7 @@ std::vector<std::string> launched;
 std::string failing;  // the call that fails next, and after how many more of it
 int failing_after, failing_with;
 thread_local cudaError_t last = cudaSuccess;
-int poke_value;  // written to poke_name by the next synchronisation
+int poke_value, poke_after;  // written to poke_name by the next synchronisation but so many
 std::string poke_name;
 
 cudaError_t result(const char* call) {
@@ -65,8 +65,10 @@ int fake_peek() { return last; }
 int fake_launches() { return (int)launched.size(); }
 const char* fake_launch(int i) { return launched[i].c_str(); }
 void fake_set(const char* name, int value) { *variable(name) = value; }
-void fake_poke_at_sync(const char* name, int value) {
+int fake_get(const char* name) { return *variable(name); }
+void fake_poke_at_sync(const char* name, int value, int after) {
   poke_name = name;
+  poke_after = after;
   poke_value = value;
 }
 
@@ -119,8 +121,8 @@ cudaError_t cudaMemcpyToSymbolAsync(const void* symbol, const void* from, size_t
 }
 cudaError_t cudaStreamSynchronize(cudaStream_t) {
   const cudaError_t e = result("sync");
-  if (e == cudaSuccess && !poke_name.empty()) {
-    *variable(poke_name) = poke_value;
+  if (e == cudaSuccess && !poke_name.empty() && poke_after-- == 0) {
+    *variable(poke_name) |= poke_value;
     poke_name.clear();
   }
   return e;

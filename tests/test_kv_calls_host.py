@@ -222,9 +222,30 @@ def test_failed_queries_launch_nothing_and_leave_nothing(fake, name, failing):
     assert call(fake, **kw) == L.MK_OK
 
 
-@pytest.mark.parametrize("failing", ["copy", "sync"])
+@pytest.mark.parametrize("failing", ["copy", "sync", "launch"])
 def test_a_failed_status_leaves_nothing(fake, failing):
     fake.fail(failing)
     assert fake.lib.mk_kv_status(None) == L.MK_ERR_CUDA
     assert fake.lib.fake_peek() == 0
     assert fake.lib.mk_kv_status(None) == L.MK_OK
+
+
+# ---- findings ----
+CONTENTS, TIMEOUT = 1, 2  # the word's bits
+
+
+@pytest.mark.parametrize("bits,status", [(0, L.MK_OK), (CONTENTS, L.MK_ERR_INVALID_ARG),
+                                         (TIMEOUT, L.MK_ERR_TIMEOUT), (3, L.MK_ERR_TIMEOUT)])
+def test_findings_are_reported_once(fake, bits, status):
+    fake.lib.fake_set(b"kv_status_word", bits)
+    assert fake.lib.mk_kv_status(None) == status
+    assert fake.lib.mk_kv_status(None) == L.MK_OK
+
+
+@pytest.mark.parametrize("found", [0, CONTENTS])
+@pytest.mark.parametrize("meanwhile", [CONTENTS, TIMEOUT])
+def test_what_another_stream_finds_meanwhile_is_kept(fake, found, meanwhile):
+    fake.lib.fake_set(b"kv_status_word", found)
+    fake.lib.fake_poke_at_sync(b"kv_status_word", meanwhile, 1)  # behind the taking
+    assert fake.lib.mk_kv_status(None) == (L.MK_ERR_INVALID_ARG if found else L.MK_OK)
+    assert fake.lib.mk_kv_status(None) == (L.MK_ERR_TIMEOUT if meanwhile == TIMEOUT else L.MK_ERR_INVALID_ARG)
