@@ -11,6 +11,6 @@ from ._lib import (MK_ABL_GRAPH, MK_ABL_PDL, MK_ABL_STREAM, MK_ERR_CUDA, MK_ERR_
                    mk_decode_step_ablation, mk_decode_step_host, mk_decode_step_noalloc, mk_destroy, mk_get_info,
                    mk_plan, mk_plan_check, mk_set_wait_timeout, mk_set_trace, mk_get_trace, mk_set_l2_prefetch, mk_set_residual_copies, mk_set_hold_policy, mk_status_string,
                    mk_sync_status, MK_SRC_BF16, MK_SRC_F32, mk_attn_decode, mk_attn_prefill,
-                   mk_attn_workspace_bytes, mk_kv_append, mk_kv_status)
+                   mk_attn_workspace_bytes, mk_kv_append, mk_kv_set_wait_timeout, mk_kv_status)
 from .cache import KVCache  # noqa: F401
 from .decoder import Decoder, desc_from_config  # noqa: F401

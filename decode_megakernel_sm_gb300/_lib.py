@@ -133,6 +133,7 @@ SIGNATURES = {
                                   C.c_void_p, C.c_size_t, C.c_void_p]),
     "mk_attn_workspace_bytes": (C.c_int, [C.c_int] * 6 + [C.POINTER(C.c_size_t)]),
     "mk_kv_status": (C.c_int, [C.c_void_p]),
+    "mk_kv_set_wait_timeout": (C.c_int, [C.c_uint64]),
     "mk_set_race_stress": (C.c_int, [C.c_void_p, C.c_uint, C.c_uint, C.c_int]),
     "mk_debug_read": (C.c_int, [C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_size_t]),
     "mk_set_poll_policy": (C.c_int, [C.c_void_p, C.c_int, C.c_uint]),
@@ -323,6 +324,10 @@ def mk_attn_workspace_bytes(decode: bool, n_tokens: int, batch: int, n_q_heads: 
     _check(lib().mk_attn_workspace_bytes(int(decode), n_tokens, batch, n_q_heads, n_kv_heads,
                                          head_dim, C.byref(n)), "mk_attn_workspace_bytes")
     return n.value
+
+
+def mk_kv_set_wait_timeout(ns: int):
+    _check(lib().mk_kv_set_wait_timeout(ns), "mk_kv_set_wait_timeout")
 
 
 def mk_kv_status(stream=None) -> int:

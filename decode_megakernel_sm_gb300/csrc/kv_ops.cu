@@ -160,6 +160,10 @@ static bool prefill_ready() {
   return true;
 }
 
+// How long a prefill block may get no further, in ns (mk_kv_set_wait_timeout).
+constexpr uint64_t WAIT_NS = 2000000000ull;
+static std::atomic<uint64_t> wait_ns{WAIT_NS};
+
 template <int D>
 static int prefill_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
   const auto enc = tensor_map_encoder();
@@ -173,6 +177,7 @@ static int prefill_launch(const AttnArgs& a, int n_sm, cudaStream_t s) {
   // (a scale of zero: the smallest number, which keeps masked scores at -inf and takes
   // finite ones to below 2^-20)
   p.scale2 = std::fmax(std::fabs(a.scale) * LOG2E, std::numeric_limits<float>::denorm_min());
+  p.wait_ns = wait_ns.load(std::memory_order_relaxed);
   p.box = a.kv.table && a.kv.block < PF_UNIT ? a.kv.block : PF_UNIT;
   CUtensorMap maps[3];
   const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)D * 2};
@@ -442,6 +447,12 @@ extern "C" int mk_attn_prefill(const mk_kv_view* kv, const mk_kv_batch* bt, int 
                                const mk_rows* q, float scale, const mk_rows* out, float* d_lse,
                                void* d_ws, size_t ws_bytes, void* stream) {
   return attention(false, kv, bt, n_q_heads, q, scale, out, d_lse, d_ws, ws_bytes, stream);
+}
+
+extern "C" int mk_kv_set_wait_timeout(uint64_t ns) {
+  if (ns > 1ull << 62) return MK_ERR_INVALID_ARG;  // (a limit is a time of the clock, in 64 bits)
+  wait_ns.store(ns == 0 ? WAIT_NS : ns, std::memory_order_relaxed);
+  return MK_OK;
 }
 
 extern "C" int mk_kv_status(void* stream) {

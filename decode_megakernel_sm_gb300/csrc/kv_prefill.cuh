@@ -51,9 +51,10 @@
 // value of a later token would still be NaN: rows whose result is not finite
 // although their weights are, are redone by attn_row.
 //
-// Every wait is bounded in time: where the block gets no further for two seconds, all
-// warps leave through the common end, which frees the tensor memory and sets the
-// status word.
+// Every wait is bounded in time: where the block gets no further for two seconds
+// (mk_kv_set_wait_timeout), all warps leave through the common end: the loaders wait
+// for their copies and the product warps for their products in flight, then the tensor
+// memory is freed and the status word set.
 #pragma once
 #include <cuda.h>
 
@@ -75,7 +76,7 @@ constexpr int PF_MIN_SHARE = 7 * PF_UNIT;
 // cost about as much.
 constexpr int PF_SNAP = 4 * PF_UNIT;
 constexpr int PF_AFTER = 1 << 30;
-constexpr unsigned long long PF_TIMEOUT_NS = 2000000000ull;
+constexpr unsigned long long PF_DRAIN_NS = 2000000000ull;  // for what is in flight at the end
 
 template <int D>
 struct PfShape {
@@ -100,6 +101,7 @@ struct PfArgs {
   int negate;    // the scale is negative: scale2 is its magnitude, Q K^T is negated
   float scale2;  // |scale| log2 e
   int box;       // rows of a TMA box
+  unsigned long long wait_ns;  // how long a block may get no further
 };
 
 // ---- the line of jobs ------------------------------------------------------
@@ -577,7 +579,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
     }
     mbar_init(smem_u32(&sh.drain), 2);
     sh.abort = 0;
-    sh.limit = gtimer() + PF_TIMEOUT_NS;
+    sh.limit = gtimer() + p.wait_ns;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), 512);
@@ -638,9 +640,9 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
             if (w.e[t] == w.ka) continue;
             if (q_used >> t & 1) {
               ok = ok && __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.q_empty[t], q_phase >> t & 1));
-              q_phase ^= 1u << t;
+              if (ok) q_phase ^= 1u << t;  // (else no load follows)
             }
-            q_used |= 1u << t;
+            if (ok) q_used |= 1u << t;
             if (ok && lane == 0) {
               const uint32_t bar = smem_u32(&sh.q_full[t]), dst = q_smem + t * Sh::TILE;
               mbar_expect_tx(bar, (uint32_t)tile_rows * D * 2);
@@ -706,19 +708,19 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
             __syncwarp();
           }
           if (!is_v && j == w.ka) walk.next(p);  // while the copy runs
-          if (!is_v && (n & 63) == 0 && lane == 0) pf_put_off(sh, PF_TIMEOUT_NS);
+          if (!is_v && (n & 63) == 0 && lane == 0) pf_put_off(sh, p.wait_ns);
         }
       }
-      if (sh.abort) {  // given up: wait for the copies in flight, again with a limit
-        const unsigned long long t0 = gtimer();
-        for (uint32_t i = n > NS ? n - NS : 0; i < n; i++)
-          while (!mbar_try(smem_u32(&full[i % NS]), (i / NS) & 1) && gtimer() - t0 < PF_TIMEOUT_NS) {
-          }
-        for (int t = 0; t < 2; t++)  // (the queries' last load has q_empty's phase)
-          while ((q_used >> t & 1) && !mbar_try(smem_u32(&sh.q_full[t]), q_phase >> t & 1) &&
-                 gtimer() - t0 < PF_TIMEOUT_NS) {
-          }
-      }
+      // The copies in flight, with a limit: nobody else may be waiting for them, since the
+      // block can give up after this warp has issued its last.
+      const unsigned long long t0 = gtimer();
+      for (uint32_t i = n > NS ? n - NS : 0; i < n; i++)
+        while (!mbar_try(smem_u32(&full[i % NS]), (i / NS) & 1) && gtimer() - t0 < PF_DRAIN_NS) {
+        }
+      for (int t = 0; t < 2; t++)  // (the queries' last load has q_empty's phase)
+        while ((q_used >> t & 1) && !mbar_try(smem_u32(&sh.q_full[t]), q_phase >> t & 1) &&
+               gtimer() - t0 < PF_DRAIN_NS) {
+        }
     } else {
       // --------------------------------------------------------- products ----
       // (the whole warp takes every step, so that addresses stay in uniform
@@ -859,7 +861,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
       if (lead) tc_commit(smem_u32(&sh.drain));
       const unsigned long long t0 = gtimer();
       while (!mbar_try(smem_u32(&sh.drain), 0))
-        if (gtimer() - t0 > PF_TIMEOUT_NS) {
+        if (gtimer() - t0 > PF_DRAIN_NS) {
           sh.abort = 1;
           break;
         }
@@ -1042,7 +1044,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
         const int hh = w.h * a.G + __shfl_sync(0xFFFFFFFFu, row_head, src);
         const long long row_tok = w.row + __shfl_sync(0xFFFFFFFFu, row_token, src);
         // (some 65 ns a cache row)
-        if (lane == 0) pf_put_off(sh, PF_TIMEOUT_NS + 1000ull * (unsigned)w.len);
+        if (lane == 0) pf_put_off(sh, p.wait_ns + 1000ull * (unsigned)w.len);
         float m1, l1, o1[D / 32];
         attn_row<D>(a.kv, w.b, w.h, (const uint16_t*)a.q.p + row_tok * a.q.ts + hh * a.q.hs,
                     a.scale, ka * PF_UNIT, min(end, kb * PF_UNIT), m1, l1, o1);

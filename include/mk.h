@@ -290,6 +290,13 @@ int mk_attn_prefill(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q_heads, 
 int mk_attn_workspace_bytes(int decode, int n_tokens, int batch, int n_q_heads, int n_kv_heads,
                             int head_dim, size_t* bytes);
 
+/* Limit, in nanoseconds, of the time that a block of mk_attn_prefill may get no
+ * further before it gives up (MK_ERR_TIMEOUT from mk_kv_status, outputs
+ * unspecified); 0: the default, 2 s.  For this process, from the next call on;
+ * a captured graph keeps the limit of its capture.  The other operators wait
+ * for nothing.  Errors: MK_ERR_INVALID_ARG (more than 2^62).               */
+int mk_kv_set_wait_timeout(uint64_t ns);
+
 /* Wait for `stream`, then return and clear, in one step, what the KV-cache
  * operators found on the current device since the last call: MK_ERR_TIMEOUT if
  * any call gave up, else MK_ERR_INVALID_ARG if any found bad contents, else

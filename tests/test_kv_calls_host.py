@@ -249,3 +249,10 @@ def test_what_another_stream_finds_meanwhile_is_kept(fake, found, meanwhile):
     fake.lib.fake_poke_at_sync(b"kv_status_word", meanwhile, 1)  # behind the taking
     assert fake.lib.mk_kv_status(None) == (L.MK_ERR_INVALID_ARG if found else L.MK_OK)
     assert fake.lib.mk_kv_status(None) == (L.MK_ERR_TIMEOUT if meanwhile == TIMEOUT else L.MK_ERR_INVALID_ARG)
+
+
+def test_wait_timeouts(fake):
+    f = fake.lib.mk_kv_set_wait_timeout
+    assert f(2 ** 62 + 1) == L.MK_ERR_INVALID_ARG
+    for ns in (2 ** 62, 1, 0):
+        assert f(ns) == L.MK_OK
