@@ -386,7 +386,9 @@ struct PfShared {
   volatile int abort;
   // When waiting ends (globaltimer): put off by the key loader as it gets on, which
   // hangs on all other roles, and by a warp that is about to redo a row.
-  unsigned long long limit;
+  // (wait_ns from the parameters at each use: 8192 tokens of 64-dim heads 260 -> 268 us,
+  // which the place of the softmax loop's code decides more than what runs.)
+  unsigned long long limit, wait_ns;
 };
 
 MK_DEV void pf_put_off(PfShared& sh, unsigned long long ns) { atomicMax(&sh.limit, gtimer() + ns); }
@@ -579,6 +581,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
     }
     mbar_init(smem_u32(&sh.drain), 2);
     sh.abort = 0;
+    sh.wait_ns = p.wait_ns;
     sh.limit = gtimer() + p.wait_ns;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -640,9 +643,9 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
             if (w.e[t] == w.ka) continue;
             if (q_used >> t & 1) {
               ok = ok && __all_sync(0xFFFFFFFFu, pf_wait(sh, &sh.q_empty[t], q_phase >> t & 1));
-              if (ok) q_phase ^= 1u << t;  // (else no load follows)
+              q_phase ^= (uint32_t)ok << t;  // (no load follows a wait that failed)
             }
-            if (ok) q_used |= 1u << t;
+            q_used |= (uint32_t)ok << t;
             if (ok && lane == 0) {
               const uint32_t bar = smem_u32(&sh.q_full[t]), dst = q_smem + t * Sh::TILE;
               mbar_expect_tx(bar, (uint32_t)tile_rows * D * 2);
@@ -708,7 +711,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
             __syncwarp();
           }
           if (!is_v && j == w.ka) walk.next(p);  // while the copy runs
-          if (!is_v && (n & 63) == 0 && lane == 0) pf_put_off(sh, p.wait_ns);
+          if (!is_v && (n & 63) == 0 && lane == 0) pf_put_off(sh, sh.wait_ns);
         }
       }
       // The copies in flight, with a limit: nobody else may be waiting for them, since the
@@ -1044,7 +1047,7 @@ kv_prefill_kernel(const __grid_constant__ PfArgs p, const __grid_constant__ CUte
         const int hh = w.h * a.G + __shfl_sync(0xFFFFFFFFu, row_head, src);
         const long long row_tok = w.row + __shfl_sync(0xFFFFFFFFu, row_token, src);
         // (some 65 ns a cache row)
-        if (lane == 0) pf_put_off(sh, p.wait_ns + 1000ull * (unsigned)w.len);
+        if (lane == 0) pf_put_off(sh, sh.wait_ns + 1000ull * (unsigned)w.len);
         float m1, l1, o1[D / 32];
         attn_row<D>(a.kv, w.b, w.h, (const uint16_t*)a.q.p + row_tok * a.q.ts + hh * a.q.hs,
                     a.scale, ka * PF_UNIT, min(end, kb * PF_UNIT), m1, l1, o1);
