@@ -256,3 +256,23 @@ def test_wait_timeouts(fake):
     assert f(2 ** 62 + 1) == L.MK_ERR_INVALID_ARG
     for ns in (2 ** 62, 1, 0):
         assert f(ns) == L.MK_OK
+
+
+def test_prefill_is_compiled_to_the_registers_that_it_deals_out():
+    """The kernel would wait for registers that its launch does not hold, so a call
+    refuses to run with any other number; the compiler's log says it beforehand."""
+    import os
+    import re
+
+    from decode_megakernel_sm_gb300 import build as B
+    L.lib()
+    log = os.path.join(B.BUILD, "kv_ops.cu.o.log")
+    if not os.path.exists(log):
+        pytest.skip("the library was not built here")
+    source = open(os.path.join(B.CSRC, "kv_prefill.cuh")).read()
+    regs, threads = (int(re.search(rf"constexpr int {n} = (\d+);", source)[1]) for n in ("PF_REGS", "PF_THREADS"))
+    dealt = [int(n) for n in re.findall(r"setmaxnreg\.(?:dec|inc)\.sync\.aligned\.u32 (\d+);", source)]
+    assert 128 * dealt[0] + (threads - 128) * dealt[1] <= regs * threads
+    used = re.findall(r"Compiling entry function '\w*kv_prefill_kernel\w*'.*?Used (\d+) registers",
+                      open(log).read(), re.S)
+    assert len(used) == 2 and all(int(n) == regs for n in used)
