@@ -69,8 +69,11 @@ constexpr int PF_REGS = 168;      // per thread at launch (setmaxnreg deals them
 constexpr int PF_ROWS = 256;      // rows of a job
 constexpr int PF_UNIT = 128;      // cache rows of a unit
 constexpr int PF_JOB_COST = 320;  // a job's start and end, in keys (measured: 2.3 to 2.6 units)
-// A part of a job is not worth less: a prompt of 1024 tokens, 8 kv heads of 64, 18.2 us
-// (a block per job) where 4 units take 20.9 (jobs cut and joined).
+// A part of a job is not worth less: a cut costs another start and end, 2.5 units, and
+// the join, 3 to 5 us with units of 1.1.  One prompt, us with 7, 6 and 5 units:
+//   32/8 heads of 64, tokens   768 18.2 18.2 17.1   960 19.1 19.1 19.9   1024 18.2 20.6 20.9
+//   16/4 heads of 128, tokens  768 21.5 21.6 20.1   960 23.9 24.0 26.2   1024 21.1 23.4 23.9
+//                             1100 26.6 28.3 27.2  1280 26.9 27.3 26.1   1500 28.7 27.1 26.8
 constexpr int PF_MIN_SHARE = 7 * PF_UNIT;
 // A cut so many keys from a job's border moves there: a partial state and its join
 // cost about as much.
@@ -167,7 +170,12 @@ MK_DEV PfLine pf_line(const PfArgs& p, int blocks, int lane, const PfSeq& s0) {
   }
   PfLine l;
   l.total = n * p.a.kv.Hkv;
-  l.parts = (int)min((long long)blocks, max((long long)jobs * p.a.kv.Hkv, l.total / PF_MIN_SHARE));
+  // As many parts as jobs while a block each is there, more where they are an eighth more:
+  // fewer move every cut for the sake of a few blocks (1100 tokens of 32/8 heads of 64,
+  // 144 jobs: 21.1 us, 22.3 as 149 parts; 2048 of 16/4 heads of 128, 128 jobs: 36.2, 34.0
+  // as 152 parts).
+  const long long all = (long long)jobs * p.a.kv.Hkv, cut = min((long long)blocks, l.total / PF_MIN_SHARE);
+  l.parts = (int)(8 * cut < 9 * all ? min((long long)blocks, all) : cut);
   if (l.parts > 0) {
     l.quot = l.total / l.parts;
     l.rest = (int)(l.total - l.quot * l.parts);

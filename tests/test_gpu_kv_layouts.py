@@ -107,3 +107,10 @@ def test_append_on_a_stream_of_its_own():
         assert torch.equal(got, want) and torch.equal(c.k, cached[0]) and torch.equal(c.v, cached[1])
         assert torch.equal(again[0], want_other[0]) and torch.equal(again[1], want_other[1])
     c.cache.check()
+
+
+@pytest.mark.parametrize("heads,tokens", [((32, 8, 64), n) for n in (950, 1090, 1150, 1200)] +
+                         [((16, 4, 128), n) for n in (1090, 2000, 2300)])
+def test_prefill_of_about_as_many_jobs_as_blocks(heads, tokens):
+    c = Case(heads, [tokens], [tokens], block=64, seed=75)
+    c.check("prefill", c.run("prefill"))
