@@ -6,8 +6,10 @@ this file.  Rebuilds only when a source or header is newer than the library.
 The same build also makes libmk_bounds.so: the C ABI and the small-model
 kernel variant (hidden 256) compiled with MK_BOUNDS defined, so that every
 checked access of the kernel records MK_ERR_BOUNDS instead of leaving its
-buffer (a stand-in for a memory checker; see mk_device.cuh).  The binding
-loads it instead of libmk.so when the environment sets MK_LIB=bounds.
+buffer (a stand-in for a memory checker; see mk_device.cuh).  The cache
+operators (kv_ops.cu) are in it for their entry points alone: they check
+lengths, offsets and block ids always, and have no checked accesses.  The
+binding loads it instead of libmk.so when the environment sets MK_LIB=bounds.
 """
 from __future__ import annotations
 
@@ -24,7 +26,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmk.so")
 LIB_BOUNDS = os.path.join(PKG, "libmk_bounds.so")
-# translation units of the bounds-checked library (the small variant only)
+# translation units of the bounds-checked library (the small variant, and the entry points
+# of the cache operators)
 BOUNDS_CU = ("api.cu", "pack.cu", "kv_ops.cu", "k_h256_d64_g2_b1.cu")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -50,9 +50,9 @@ static cudaError_t launch(bool early, void (*kernel)(P...), dim3 grid, unsigned 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Four tokens to a block keep more loads in flight for one look-up (25 us against 33
-// with one, 9833 tokens of 48 heads of 64); one token to a block starts sooner (3.2 us
-// against 4.1 for a single token), so few tokens take that.
+// Four tokens to a block keep more loads in flight for one look-up (24.6 us against 33.9
+// with one, 11198 tokens of 48 heads of 64); one token to a block starts sooner (3.1 us
+// against 3.9 for a single token), so few tokens take that.
 template <int D, bool F32>
 static cudaError_t append_launch(const AppendArgs& a, int n_sm, cudaStream_t s) {
   constexpr int NT = KV_APPEND_TOKENS;

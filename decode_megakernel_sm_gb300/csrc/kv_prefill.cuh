@@ -30,12 +30,15 @@
 //
 // Bound: with 128-dim heads the tensor cores (4 D operations a pair; 8192 tokens of
 // 16 heads, 275 GFLOP, take 183 us: 1.50 PFLOP/s, 0.78 of a measured GEMM's rate),
-// with 64-dim heads the softmax (8192 tokens of 32 heads: 257 us, 1.07 PFLOP/s).
-// A unit of two tiles has 32768 pairs: their exponentials take an SM 1040 cycles,
-// their scaling, sums, maxima and rounding as many on other pipes; the softmax warps
-// alone took 1625, with the products beside them about 2100.  Short prompts are
-// bound by the start (3 us of look-ups, 2.5 units a job) and the joins (5 of 84 us
-// for eight prompts of 512-2048 tokens).
+// with 64-dim heads the chain of steps of the softmax warps (8192 tokens of 32 heads:
+// 257 us, 1.07 PFLOP/s).  A unit of two tiles has 32768 pairs: their exponentials take
+// an SM 1040 cycles, their scaling, sums, maxima and rounding as many on other pipes;
+// the softmax warps alone took 1625, with the products beside them about 2100, and no
+// pipe is full (eight prompts of 512-2048 tokens: exponentials 0.34 of the active
+// cycles, products 0.33, issue slots 0.43).  Short prompts are bound by the start (3 us
+// of look-ups), the jobs' starts and ends (2.5 units a job: 20 of the 72 units of those
+// eight prompts' blocks) and the joins (4 of their 84 us).  Where the compiler puts the
+// softmax loop moves the times of 64-dim heads by up to 4 % (257 to 268 us).
 //
 // The line's measure is keys: a job costs its visible rows and PF_JOB_COST for
 // its start and end, and is cut wherever an equal share of the whole ends (or
@@ -394,8 +397,8 @@ struct PfShared {
   volatile int abort;
   // When waiting ends (globaltimer): put off by the key loader as it gets on, which
   // hangs on all other roles, and by a warp that is about to redo a row.
-  // (wait_ns from the parameters at each use: 8192 tokens of 64-dim heads 260 -> 268 us,
-  // which the place of the softmax loop's code decides more than what runs.)
+  // (wait_ns from the parameters at each use instead: 8192 tokens of 64-dim heads 261 ->
+  // 268 us, by the place of the code alone.)
   unsigned long long limit, wait_ns;
 };
 
