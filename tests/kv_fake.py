@@ -13,7 +13,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 def _compiled():
     """Its library, built where a source is newer."""
     out = os.path.join(B.BUILD, "fake")
-    so, obj = os.path.join(out, "libkv_fake.so"), os.path.join(out, "kv_ops.o")
+    so, obj = os.path.join(out, "libkv_fake.so"), os.path.join(out, f"kv_ops.{os.getpid()}.o")
     fake = os.path.join(HERE, "fake_cudart.cpp")
     if os.path.exists(so) and all(os.path.getmtime(f) <= os.path.getmtime(so) for f in B._deps() + [fake, __file__]):
         return so
@@ -28,6 +28,7 @@ def _compiled():
                     os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
                     fake, obj, "-o", tmp], check=True)
     os.replace(tmp, so)
+    os.remove(obj)
     return so
 
 
