@@ -65,6 +65,7 @@
 
 #include "attn_tc.cuh"
 #include "kv_attn.cuh"
+#include "kv_tile_ring.h"
 #include "mk_tc.cuh"
 
 namespace mk {
@@ -637,7 +638,7 @@ MK_DEV void pf_block(const PfArgs& p, const CUtensorMap& kmap, const CUtensorMap
       bool ok = true;
       PfRec w;
       uint32_t q_used = 0, q_phase = 0;  // by tile: loaded before; phase of q_empty
-      uint32_t tiles = 0, wide = 0;      // Q8: tiles so far; by stage: whether its last one was loaded whole
+      TileRing<NS> tiles;                // Q8: loaded whole, or to be made of codes
       int fresh = 0;                     // the job's first unit of new tokens' rows alone
       if (Q8 && p.widened) pdl_wait();   // (the rows that a kernel before this one widens)
       PfWalk walk;
@@ -711,15 +712,15 @@ MK_DEV void pf_block(const PfArgs& p, const CUtensorMap& kmap, const CUtensorMap
           const int blk = ahead;
           if (j + 1 < kb) ahead = lookup(j + 1);
           if constexpr (Q8) {
-            const uint32_t tile = tiles++, ts = tile % NS;
-            wide &= ~(1u << ts);
             // (A wait can tell a phase of a barrier from the next one alone, so whoever waits for
             // tiles to be free waits for every one: where tiles of both kinds alternate that is this
             // warp, before their codes, too, else the warps that make them.)
-            if (p.widened && tile >= NS) ok = __all_sync(0xFFFFFFFFu, pf_wait(sh, &empty[ts], tile / NS - 1));
+            uint32_t ts;
+            ok = tiles.take(p.widened != 0,
+                            [&](uint32_t s, uint32_t use) { return __all_sync(0xFFFFFFFFu, pf_wait(sh, &empty[s], use)); }, ts);
             if (!ok) break;
             if (pf8_whole(p, w, fresh, j)) {  // from the rows that are bf16 already
-              wide |= 1u << ts;
+              tiles.copies(ts);
               const uint32_t bar = smem_u32(&full[ts]);
               if (lane == 0) {
                 mbar_expect_tx(bar, Sh::TILE);
@@ -822,10 +823,10 @@ MK_DEV void pf_block(const PfArgs& p, const CUtensorMap& kmap, const CUtensorMap
       // block can give up after this warp has issued its last.
       const unsigned long long t0 = gtimer();
       if constexpr (Q8) {
-        for (uint32_t i = tiles > NS ? tiles - NS : 0; i < tiles; i++)
-          while ((wide >> i % NS & 1) && !mbar_try(smem_u32(&full[i % NS]), (i / NS) & 1) &&
-                 gtimer() - t0 < PF_DRAIN_NS) {
+        tiles.drain([&](uint32_t s, uint32_t use) {
+          while (!mbar_try(smem_u32(&full[s]), use & 1) && gtimer() - t0 < PF_DRAIN_NS) {
           }
+        });
         full = sh8.full[is_v];
       }
       constexpr uint32_t STAGES = Q8 ? Sh8::STAGES : NS;
