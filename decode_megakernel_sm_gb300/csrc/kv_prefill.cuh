@@ -608,6 +608,10 @@ MK_DEV void pf_block(const PfArgs& p, const CUtensorMap& kmap, const CUtensorMap
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc(smem_u32(&sh.tmem), 512);
+  if (Q8 && p.widened) {  // a kernel before this one widens rows: its time is none of this block's
+    pdl_wait();
+    if (threadIdx.x == 0) sh.limit = gtimer() + p.wait_ns;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -640,7 +644,6 @@ MK_DEV void pf_block(const PfArgs& p, const CUtensorMap& kmap, const CUtensorMap
       uint32_t q_used = 0, q_phase = 0;  // by tile: loaded before; phase of q_empty
       TileRing<NS> tiles;                // Q8: loaded whole, or to be made of codes
       int fresh = 0;                     // the job's first unit of new tokens' rows alone
-      if (Q8 && p.widened) pdl_wait();   // (the rows that a kernel before this one widens)
       PfWalk walk;
       if (!is_v) {
         walk.begin(p, blockIdx.x, lane);
