@@ -359,7 +359,8 @@ int mk_attn_int8_workspace_bytes(int decode, int n_tokens, int batch, int n_q_he
 /* Limit, in nanoseconds, of the time that a block of mk_attn_prefill or
  * mk_attn_prefill_int8, or a warp of mk_attn_decode_int8, may get no further before
  * it gives up (MK_ERR_TIMEOUT from mk_kv_status, outputs unspecified); 0: the
- * default, 2 s.  For this process, from the next call on; a captured graph keeps the
+ * default, 2 s.  A prefill block looks at the time every 0.3 ms, a decode warp at
+ * every try.  For this process, from the next call on; a captured graph keeps the
  * limit of its capture.  The other operators wait for nothing.  Errors:
  * MK_ERR_INVALID_ARG (more than 2^62).                                      */
 int mk_kv_set_wait_timeout(uint64_t ns);
