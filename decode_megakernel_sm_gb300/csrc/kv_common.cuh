@@ -6,10 +6,11 @@
 
 namespace mk {
 
-// Programmatic dependent launch: the kernels that join partial states start while the
-// one that makes them still runs, and wait for all of its work before they read any.
-// The others start plainly: on an idle stream, where a caller's every launch finds it,
-// the early start costs 3 to 10 us more than it saves.
+// Programmatic dependent launch: a call's later kernels (those that join partial states,
+// and the prefill behind the one that widens an 8-bit cache's rows for it) start while
+// the one before still runs, and wait for all of its work before they read any.
+// A call's first kernel starts plainly: on an idle stream, where a caller's every launch
+// finds it, the early start costs 3 to 10 us more than it saves.
 MK_DEV void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
 MK_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
