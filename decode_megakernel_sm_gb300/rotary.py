@@ -58,3 +58,10 @@ class Rotary:
         self._held = (C.c_double * (dims // 2))(*frequencies)  # what the calls read
         self._packed = _ROTARY.pack(dims, int(self.interleaved), C.addressof(self._held) if dims else 0,
                                     self.magnitude)
+
+    def __reduce__(self):  # copies pack the address of their own numbers
+        return _again, (self.head_dim, self.dims, self.interleaved, self.magnitude, self.frequencies)
+
+
+def _again(head_dim, dims, interleaved, magnitude, frequencies):
+    return Rotary(head_dim, dims=dims, interleaved=interleaved, magnitude=magnitude, frequencies=frequencies)
