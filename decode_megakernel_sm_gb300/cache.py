@@ -31,6 +31,13 @@ def _call(name):
     return f
 
 
+def _again(k, v, table, scales, unusable):
+    cache = KVCache(k, v, table, scales)
+    if unusable:
+        cache._read_as(None, k.shape, unusable)
+    return cache
+
+
 class KVCache:
     """k, v: bf16 CUDA tensors.  With table (int32 [batch][stride], contiguous):
     pools [n_blocks][kv heads][block][head_dim], row p of sequence b in block
@@ -104,6 +111,9 @@ class KVCache:
         self.table = table
         self._view = _VIEW.pack(self.k.data_ptr(), self.v.data_ptr(), n_blocks, self.heads, block,
                                 self.dim, tp, stride)
+
+    def __reduce__(self):  # copies pack the addresses of their own tensors
+        return _again, (self.k, self.v, self.table, self.scales, self._unusable)
 
     # -- marshalling --------------------------------------------------------
     def _rows(self, t, name, dtype, n, heads):
