@@ -238,6 +238,7 @@ class KVCache:
     def _ex(self, theta, rotary, q_norm, k_norm, eps):
         """(Rotary or None, mk_head_norm or None) of an append."""
         if rotary is None:
+            theta = float(theta)  # (kept by value: a tensor's or an array's may change)
             rotary = _rotaries.get((self.dim, theta))
             if rotary is None and theta != 0:
                 if len(_rotaries) >= 64:

@@ -34,6 +34,7 @@ class Rotary:
         if (theta is None) == (frequencies is None):
             raise ValueError("expected theta or frequencies")
         if frequencies is None:
+            theta = float(theta)
             if not (1.0 <= theta <= 1e30):
                 raise ValueError("theta: expected a number from 1 to 1e30")
             if not (1.0 <= factor < math.inf):
