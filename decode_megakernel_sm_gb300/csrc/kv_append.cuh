@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(KV_APPEND_THREADS) kv_append_kernel(const __gr
 #pragma unroll
   for (int e = 0; e < 8; e++) z[e] = a.rotate ? cs[w][t + e] : make_float2(1.f, 0.f);
   const int heads = a.Hq + 2 * a.kv.Hkv;  // of q, then of k, then of v
+  const int turning = a.rotate ? a.Hq + a.kv.Hkv : 0;
   for (int h0 = threadIdx.x / PIECES % HL; h0 < heads; h0 += HL * U) {
     Eight<F32> lo[U], hi[U];
 #pragma unroll
@@ -137,13 +138,13 @@ __global__ void __launch_bounds__(KV_APPEND_THREADS) kv_append_kernel(const __gr
       lo[u].get(f);
       hi[u].get(g);
       uint16_t* dst = (uint16_t*)a.qo.p + token * a.qo.ts + h * a.qo.hs;
-      bool turn = true;
+      const bool turn = h < turning;
       if (h >= a.Hq) {
         if (row < 0) continue;  // no page
         h -= a.Hq;
-        turn = h < a.kv.Hkv;
-        if (!turn) h -= a.kv.Hkv;
-        dst = (uint16_t*)(turn ? a.kv.k : a.kv.v) + (row + (long long)h * a.kv.block) * D;
+        const bool key = h < a.kv.Hkv;
+        if (!key) h -= a.kv.Hkv;
+        dst = (uint16_t*)(key ? a.kv.k : a.kv.v) + (row + (long long)h * a.kv.block) * D;
       }
       if (turn) {
 #pragma unroll
