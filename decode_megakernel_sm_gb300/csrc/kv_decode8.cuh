@@ -8,15 +8,16 @@
 // at once here: a warp has a ring of stages of its own, four lanes start a bulk copy each of 32
 // rows' codes and group bytes (where these are not whole 16 bytes, lanes copy them piece by
 // piece), and all arrives on one barrier.  Loads into registers, as in the bf16 kernel, took 253 us
-// for 32 sequences of 16384-32768 rows, 8 kv heads of 64; this takes 204, 4.2 TB/s, and 182 with 4
-// heads of 128, 4.4 TB/s.  What bounds it now is the chain of dependent instructions: four warps to a
+// for 32 sequences of 16384-32768 rows, 8 kv heads of 64; this takes 205, 4.2 TB/s, and 181 with 4
+// heads of 128, 4.5 TB/s.  What bounds it now is the chain of dependent instructions: four warps to a
 // scheduler issue in 0.6 of its cycles.  (Three blocks of more registers and deeper rings 229 where
 // four took 219; five 206 where four took 202.)  (Weights as bf16 alone, without the
 // remainder: 196 and 174, but twice the error where few of them count.)
 //
 // A warp waits for its own copies alone, for as long as the limit says (mk_kv_set_wait_timeout);
 // then it goes on without them and without any more, the status word is set, and at the end it
-// waits (with a limit again) for those in flight.
+// waits (with a limit again) for those in flight.  Most copies are there a step before: of a
+// cache that L2 holds few calls wait 1 ns, of a larger one nearly all do somewhere.
 #pragma once
 #include "kv_decode.cuh"
 

@@ -20,7 +20,8 @@ class Rotary:
     over it: pairs of at least ``high`` turns stay as they are, pairs of at most ``low``
     are divided by factor, those between in proportion:
         f' = (w + (1 - w) / factor) f,   w = (turns - low) / (high - low) cut to [0, 1].
-    ``frequencies`` given: these instead, dims / 2 radians per position."""
+    ``frequencies`` given: these instead, dims / 2 radians per position; so for every other
+    rule (a w that is linear in the pair's index t is not the one above)."""
 
     __slots__ = ("head_dim", "dims", "interleaved", "magnitude", "frequencies", "_held", "_packed")
 

@@ -272,8 +272,8 @@ int mk_kv_append(const mk_kv_view* kv, const mk_kv_batch* bt, int n_q_heads, con
  *     (n_blocks * n_kv_heads * block).
  * scale and scale * log2 e are finite.  out, d_lse and d_ws share no memory with one another, q or the
  * cache (MK_ERR_INVALID_ARG; interleaved rows as above).  A call whose work cannot be numbered in 31
- * bits (decode: batch * n_q_heads, or items of 64 rows when every sequence has
- * all the rows that the view can hold) is MK_ERR_UNSUPPORTED.
+ * bits (decode: batch * n_q_heads, or items of 64 rows, 128 of an 8-bit cache, when
+ * every sequence has all the rows that the view can hold) is MK_ERR_UNSUPPORTED.
  * d_ws: device scratch of at least mk_attn_workspace_bytes() bytes, 256-byte
  * aligned, for this call alone until it has run: calls that may overlap, and
  * graphs that may replay at the same time, need their own.  Its contents do
