@@ -55,11 +55,18 @@ class Rotary:
                 raise ValueError("factor and trained go with theta")
             if len(frequencies) != dims // 2 or not all(abs(f) <= math.pi for f in frequencies):
                 raise ValueError(f"frequencies: expected {dims // 2} numbers within [-pi, pi]")
-        self.head_dim, self.dims, self.interleaved = head_dim, dims, bool(interleaved)
-        self.magnitude, self.frequencies = float(magnitude), tuple(frequencies)
-        self._held = (C.c_double * (dims // 2))(*frequencies)  # what the calls read
-        self._packed = _ROTARY.pack(dims, int(self.interleaved), C.addressof(self._held) if dims else 0,
-                                    self.magnitude)
+        magnitude, frequencies = float(magnitude), tuple(float(f) for f in frequencies)
+        held = (C.c_double * (dims // 2))(*frequencies)  # what the calls read
+        packed = _ROTARY.pack(dims, bool(interleaved), C.addressof(held) if dims else 0, magnitude)
+        for name, value in zip(self.__slots__, (head_dim, dims, bool(interleaved), magnitude, frequencies,
+                                                held, packed)):
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("Rotary: cannot be changed, make another one")
+
+    def __delattr__(self, name):
+        raise AttributeError("Rotary: cannot be changed, make another one")
 
     def __reduce__(self):  # copies pack the address of their own numbers
         return _again, (self.head_dim, self.dims, self.interleaved, self.magnitude, self.frequencies)
